@@ -100,6 +100,7 @@ def library(path: Optional[str] = None):
     lib.hclrmix_last_error.argtypes = []
     lib.hclrmix_version.restype = ctypes.c_char_p
     lib.hclrmix_version.argtypes = []
+    ffn.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -320,3 +321,15 @@ def block(streams, norm_scale, down_weight, up_weight, inject_weight, prev_block
     hclrmix_run(streams, norm_scale, down_weight, up_weight, inject_weight, prev_block_output,
                 prev_post_gate, pre, post, so, workspace, prob, attrs)
     return pre, post, so
+
+
+from . import ffn  # noqa: E402
+from .ffn import (  # noqa: E402
+    ACTIVATIONS, GATE_ELEMENT, GATE_NONE, GATE_ROW, MAX_ROWS, NORM_MAX_HIDDEN, PRODUCT_MAX_WIDTH, NormProblem, Product,
+    glu, glu_backward, glu_workspace_size, hclrmix_glu, hclrmix_glu_backward, hclrmix_glu_backward_workspace_size,
+    hclrmix_glu_workspace_size, hclrmix_linear, hclrmix_linear_backward, hclrmix_linear_backward_workspace_size,
+    hclrmix_linear_workspace_size, hclrmix_residual_norm, hclrmix_residual_norm_backward,
+    hclrmix_residual_norm_workspace_size, linear, linear_backward, linear_workspace_size, residual_norm,
+    residual_norm_backward, residual_norm_workspace_size)
+
+EXPORTED = EXPORTED + ffn.EXPORTED

@@ -13,6 +13,7 @@
 
 #include "../../include/hclrmix.h"
 #include "hc_internal.h"
+#include "hc_status.h"
 
 // Scratch of hclrmix_run_noalloc: a static device array, one copy per GPU
 // (zero-filled when the code object is loaded). Host code never uses this
@@ -20,8 +21,10 @@
 static __device__ __align__(256) unsigned char scratch[HCLRMIX_NOALLOC_SCRATCH_BYTES];
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+namespace hc {
 
 hclrmix_status fail(hclrmix_status st, const char* fmt, ...) {
   char buf[512];
@@ -37,6 +40,15 @@ hclrmix_status ok() {
   g_last_error.clear();
   return HCLRMIX_OK;
 }
+
+}  // namespace hc
+
+namespace {
+
+using hc::fail;
+using hc::ok;
+using hc::overlaps;
+using hc::Range;
 
 size_t elem_size(int dtype) { return dtype == HCLRMIX_F32 ? 4 : 2; }
 
@@ -122,15 +134,6 @@ hclrmix_status resolve_path(const hclrmix_problem* p, const Dims& d, int* path) 
 }
 
 bool aligned16(const void* p) { return p == nullptr || ((uintptr_t)p & 15u) == 0; }
-
-struct Range {
-  const char* name;
-  uintptr_t lo, hi;
-};
-
-bool overlaps(const Range& a, const Range& b) {
-  return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
-}
 
 }  // namespace
 

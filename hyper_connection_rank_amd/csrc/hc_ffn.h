@@ -1,0 +1,203 @@
+// Internal interfaces of the feed-forward operators: the norms around a block
+// (hc_norm.hip), the matrix products (hc_gemm.hip) and their activations
+// (shared by the products' epilogues and the element-wise backward kernels).
+#pragma once
+
+#include "hc_device.h"
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace hc {
+
+// ------------------------------------------------------------------ activations
+
+enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4, ACT_SIGMOID = 5 };
+
+constexpr float GELU_C = 0.7978845608028654f;   // sqrt(2 / pi)
+constexpr float GELU_A = 0.044715f;
+constexpr float RSQRT2 = 0.7071067811865476f;
+constexpr float RSQRT2PI = 0.3989422804014327f;
+
+// act(x). GELU as x * erfc(-x / sqrt 2) / 2 and GELU_TANH as
+// x * sigmoid(2 t), which equal the usual forms and keep their relative
+// accuracy for negative x, where 1 + erf and 1 + tanh cancel.
+__device__ __forceinline__ float act_f(int kind, float x) {
+  switch (kind) {
+    case ACT_RELU: return x > 0.0f ? x : (x <= 0.0f ? 0.0f : x);  // NaN stays NaN
+    case ACT_SILU: return x * sigmoid(x);
+    case ACT_GELU: return 0.5f * x * erfcf(-x * RSQRT2);
+    case ACT_GELU_TANH: return x * sigmoid(2.0f * GELU_C * (x + GELU_A * x * x * x));
+    case ACT_SIGMOID: return sigmoid(x);
+    default: return x;
+  }
+}
+
+// act(x) and its derivative d.
+__device__ __forceinline__ float act_df(int kind, float x, float& d) {
+  switch (kind) {
+    case ACT_RELU:
+      d = x > 0.0f ? 1.0f : 0.0f;
+      return act_f(ACT_RELU, x);
+    case ACT_SILU: {
+      const float s = sigmoid(x);
+      d = s * (1.0f + x * (1.0f - s));
+      return x * s;
+    }
+    case ACT_GELU: {
+      const float phi = 0.5f * erfcf(-x * RSQRT2);
+      d = phi + x * (expf(-0.5f * x * x) * RSQRT2PI);
+      return x * phi;
+    }
+    case ACT_GELU_TANH: {
+      // 1 - tanh(t)^2 = 4 s (1 - s) with s = sigmoid(2 t).
+      const float s = sigmoid(2.0f * GELU_C * (x + GELU_A * x * x * x));
+      d = s + 2.0f * x * s * (1.0f - s) * GELU_C * (1.0f + 3.0f * GELU_A * x * x);
+      return x * s;
+    }
+    case ACT_SIGMOID: {
+      const float s = sigmoid(x);
+      d = s * (1.0f - s);
+      return s;
+    }
+    default: d = 1.0f; return x;
+  }
+}
+
+// ------------------------------------------------------------------ element access
+
+// Four and eight elements from any element-aligned address, n of them valid
+// (the others read as 0). ALN: every address is 16-byte aligned (four 16-bit
+// elements: 8-byte) and n is always the full count.
+typedef unsigned u32x4_h __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned u32x4_w __attribute__((ext_vector_type(4), aligned(4)));
+
+template <DT D, bool ALN> __device__ __forceinline__ uint4 ld16(const void* p) {
+  if constexpr (ALN) return *(const uint4*)p;
+  else if constexpr (D == DT::F32) return to_uint4(*(const u32x4_w*)p);
+  else return to_uint4(*(const u32x4_h*)p);
+}
+template <DT D, bool ALN> __device__ __forceinline__ void st16(void* p, uint4 v) {
+  if constexpr (ALN) *(uint4*)p = v;
+  else if constexpr (D == DT::F32) *(u32x4_w*)p = to_u32x4(v);
+  else *(u32x4_h*)p = to_u32x4(v);
+}
+
+template <DT D, bool ALN>
+__device__ __forceinline__ void load8(const void* base, int64_t i, int n, float* x) {
+  if constexpr (D == DT::F32) {
+    const float* p = (const float*)base + i;
+    if (ALN || n >= 8) {
+      const f32x4 a = __builtin_bit_cast(f32x4, to_u32x4(ld16<D, ALN>(p)));
+      const f32x4 b = __builtin_bit_cast(f32x4, to_u32x4(ld16<D, ALN>(p + 4)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = a[e];
+        x[4 + e] = b[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = e < n ? p[e] : 0.0f;
+    }
+  } else {
+    const uint16_t* p = (const uint16_t*)base + i;
+    if (ALN || n >= 8) {
+      unpack8<D>(ld16<D, ALN>(p), x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = e < n ? widen<D>(p[e]) : 0.0f;
+    }
+  }
+}
+
+// Rounds eight values to T and stores the first n.
+template <DT D, bool ALN>
+__device__ __forceinline__ void store8(void* base, int64_t i, int n, const float* x) {
+  if constexpr (D == DT::F32) {
+    float* p = (float*)base + i;
+    if (ALN || n >= 8) {
+      st16<D, ALN>(p, to_uint4(__builtin_bit_cast(u32x4, f32x4{x[0], x[1], x[2], x[3]})));
+      st16<D, ALN>(p + 4, to_uint4(__builtin_bit_cast(u32x4, f32x4{x[4], x[5], x[6], x[7]})));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) p[e] = x[e];
+    }
+  } else {
+    uint16_t* p = (uint16_t*)base + i;
+    if (ALN || n >= 8) {
+      st16<D, ALN>(p, pack8<D>(x));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) p[e] = (uint16_t)to_bits<D>(x[e]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ norms
+
+struct NormArgs {
+  const void *y, *res, *gate, *post, *pre;  // res: the residual (forward) or residual_out (backward)
+  const void *dres, *dn;                    // backward: gradients of residual_out and normed, or null
+  void *res_out, *normed;                   // forward
+  void *dy, *d_residual, *d_gate;           // backward, each or null
+  float* partial;                           // backward: [G][2][hidden] sums of the scales' gradients, or null
+  int64_t rows, gate_stride;
+  int hidden, gate_kind, post_norm;
+  float alpha, eps;
+};
+
+hipError_t launch_norm(const NormArgs& a, int dtype, bool aligned, hipStream_t s);
+// Workgroups of the backward kernel, each with one row of partial sums.
+int norm_backward_groups(int64_t rows);
+hipError_t launch_norm_backward(const NormArgs& a, int dtype, bool aligned, int groups, hipStream_t s);
+
+// out[b][c] = T(sum over r, ascending, of partial[r][b * cols + c]) for b < 2 with
+// out[b] not null; partial is [nrows][2 * cols] (or [nrows][cols] with out[1]
+// null and pitch = cols).
+hipError_t launch_column_sums(const float* partial, int nrows, int64_t pitch, int64_t cols, void* out0, void* out1,
+                              int dtype, hipStream_t s);
+
+// ------------------------------------------------------------------ products
+
+// One product out[m][n] = epilogue(sum over k of P(m, k) Q(k, n)) or a pair of
+// them. P(m, k) is p[m * ldp + k], or p[k * ldp + m] with p_trans; Q(k, n) is
+// q[k * ldq + n], or q[n * ldq + k] with q_trans.
+//   pairs = 1: one product.
+//   segments = 2: out = P0 Q0 + P1 Q1 (one sum over both contractions).
+//   batch = 2: two products out[b] = P_b Q_b in one launch.
+//   dual: g = P0 Q0 + bias0, u = P0 Q1 + bias1, out[0] = act(g) * u.
+struct Product {
+  const void* p[2];
+  const void* q[2];
+  int64_t ldp, ldq, ldr;
+  int64_t M;
+  int N, K;
+  bool p_trans, q_trans, dual;
+  int segments, batch;
+  const void* bias[2];
+  const void* residual;
+  void* out[2];   // [M, N] contiguous
+  void* save[2];  // pre-activations [M, N] (dual: g and u), or null
+  int act;
+};
+
+// Bytes of split-sum scratch a product may use (without the counters).
+size_t product_scratch(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch);
+// scratch: product_scratch() bytes; counters: HCLRMIX_COUNTER_BYTES, zero.
+hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* counters, hipStream_t s);
+
+// dz = dy * act'(p) [rows, cols], and per-group column sums of dz before its
+// rounding into partial [G][cols] (G = grad_groups(rows); null: not wanted).
+// Glu form (u not null): d0 = dy * u * act'(p), d1 = dy * act(p), partial
+// [G][2 * cols]. d0 and d1 may be null (only sums wanted).
+int grad_groups(int64_t rows);
+hipError_t launch_act_grad(const void* dy, const void* p, const void* u, void* d0, void* d1, float* partial,
+                           int64_t rows, int64_t cols, int act, int dtype, bool aligned, hipStream_t s);
+
+// Writes zeros (n bytes, a multiple of 2).
+hipError_t launch_zero(void* p, size_t n, hipStream_t s);
+
+}  // namespace hc

@@ -288,6 +288,175 @@ hclrmix_status hclrmix_run_noalloc(const void* streams, const void* norm_scale, 
 hclrmix_status hclrmix_inv_rms(const void* x, float* out, int64_t rows, int64_t dim, int32_t dtype, float eps,
                                void* stream);
 
+/* ------------------------------------------------------------------------
+ * What stands between two hyper-connection blocks: the norms around a block,
+ * its gated feed-forward product, and the matrix product with its epilogue,
+ * each with its gradients. The entry points below follow the rules above:
+ * caller-owned device memory of element type T (fp32, fp16 or bf16), checks
+ * on the host before anything is launched, work enqueued on `stream` only,
+ * nothing allocated, no state kept. Products, sums, norms and activations
+ * are taken in fp32; each output is rounded once to T (the two backward
+ * passes of products also round their pre-activation gradients to T, see
+ * there). Every sum has a fixed order: a call repeated with the same
+ * arguments gives the same bits. That order may depend on the row count (how
+ * a product is split), so unlike hclrmix_run's, a row's last bits may change
+ * with the number of rows in the call.
+ *  - Matrices are row-major. Where a problem carries a *_stride it is the
+ *    number of elements from one row to the next (at least the row's length;
+ *    0 means contiguous rows); every other tensor is contiguous. Tensors need
+ *    only their element's alignment; rows that are 16-byte aligned (address,
+ *    stride and length) run faster.
+ *  - A workspace is one like hclrmix_run's: zero-filled once before its first
+ *    use, then shared by any calls of the library that do not overlap. Its
+ *    first 4 KB hold arrival counters, left at zero by every call that
+ *    completes. Calls that may overlap (two streams, two captured graphs
+ *    replayed at once) need a workspace each.
+ *  - The calling thread's current device must be the device of `stream`.
+ *  - Errors: INVALID_ARGUMENT for a NULL required pointer or problem, a
+ *    negative size or one below its minimum, a stride below the row's length,
+ *    a non-finite attribute, a reserved field that is not 0, an unknown gate
+ *    or activation, or an output that overlaps any other buffer; UNSUPPORTED
+ *    for an unknown dtype, a size beyond the stated limits, or a pointer not
+ *    aligned to its element (a workspace: to 16 bytes); WORKSPACE_TOO_SMALL;
+ *    DEVICE. On an error nothing is launched. */
+
+#define HCLRMIX_MAX_ROWS (1 << 21)  /* rows of one call of the operators below */
+
+/* Norms before and after a block, fused with the block's gate and residual
+ * scale. For each row of y (the block's output) and residual:
+ *   z            = (post_norm ? y / rms(y) : y) * post_scale
+ *   residual_out = residual + alpha * gate * z
+ *   normed       = residual_out / rms(residual_out) * pre_scale
+ *   rms(v)       = sqrt(mean_h(v^2) + epsilon)
+ * normed is taken from residual_out before its rounding. A NULL post_scale or
+ * pre_scale counts as ones, a NULL residual as zeros. */
+typedef enum {
+  HCLRMIX_GATE_NONE = 0,    /* gate = 1; the pointer must be NULL */
+  HCLRMIX_GATE_ROW = 1,     /* one value per row, gate_stride elements apart (a column of hclrmix_run's post_gate) */
+  HCLRMIX_GATE_ELEMENT = 2  /* [rows, hidden], contiguous */
+} hclrmix_gate;
+
+typedef struct {
+  int64_t rows;         /* product of the leading dimensions; 0 is allowed */
+  int64_t hidden;       /* row length, 1 to HCLRMIX_NORM_MAX_HIDDEN */
+  int64_t gate_stride;  /* GATE_ROW: elements between rows of gate (>= 1; 0 means 1); otherwise 0 */
+  int32_t dtype;        /* hclrmix_dtype */
+  int32_t gate;         /* hclrmix_gate */
+  int32_t post_norm;    /* 1: divide y by its rms; 0: take y as it is */
+  int32_t reserved;     /* must be 0 */
+  float alpha;          /* residual scale */
+  float epsilon;        /* >= 0 */
+} hclrmix_norm_problem;
+
+#define HCLRMIX_NORM_MAX_HIDDEN 32768
+
+/* residual [rows, hidden] or NULL; gate by problem->gate; post_scale and
+ * pre_scale [hidden] or NULL; residual_out [rows, hidden]; normed
+ * [rows, hidden] or NULL (then only residual_out is written, and pre_scale
+ * must be NULL). One kernel, no workspace. rows == 0 returns OK. */
+hclrmix_status hclrmix_residual_norm(const void* y, const void* residual, const void* gate, const void* post_scale,
+                                     const void* pre_scale, void* residual_out, void* normed,
+                                     const hclrmix_norm_problem* problem, void* stream);
+
+/* Workspace of hclrmix_residual_norm_backward (partial sums of the two
+ * scales' gradients). */
+hclrmix_status hclrmix_residual_norm_workspace_size(const hclrmix_norm_problem* problem, size_t* bytes);
+
+/* Gradients of hclrmix_residual_norm. Inputs: y, gate, post_scale, pre_scale
+ * as given forward; residual_out as the forward call wrote it (the norm
+ * after the block is recomputed from it); d_residual_out and d_normed, the
+ * gradients of the two outputs, either of which may be NULL (zeros; with
+ * d_normed NULL, pre_scale and d_pre_scale must be NULL too).
+ * Outputs, each NULL when not wanted: dy [rows, hidden]; d_residual
+ * [rows, hidden]; d_gate, [rows] contiguous or [rows, hidden] by
+ * problem->gate (must be NULL without a gate); d_post_scale and d_pre_scale
+ * [hidden], sums over the rows (with rows == 0: zeros). At least one. */
+hclrmix_status hclrmix_residual_norm_backward(const void* y, const void* residual_out, const void* gate,
+                                              const void* post_scale, const void* pre_scale,
+                                              const void* d_residual_out, const void* d_normed, void* dy,
+                                              void* d_residual, void* d_gate, void* d_post_scale, void* d_pre_scale,
+                                              void* workspace, size_t workspace_bytes,
+                                              const hclrmix_norm_problem* problem, void* stream);
+
+/* Activations. GELU is x * Phi(x) (the error function); GELU_TANH its usual
+ * tanh approximation; SILU x * sigmoid(x). */
+typedef enum {
+  HCLRMIX_ACT_NONE = 0,
+  HCLRMIX_ACT_RELU = 1,
+  HCLRMIX_ACT_SILU = 2,
+  HCLRMIX_ACT_GELU = 3,
+  HCLRMIX_ACT_GELU_TANH = 4,
+  HCLRMIX_ACT_SIGMOID = 5
+} hclrmix_activation;
+
+/* Sizes of a matrix product x [rows, in] @ weight [in, out]. in and out are
+ * 1 to HCLRMIX_PRODUCT_MAX_WIDTH, strides at most that, rows at most
+ * HCLRMIX_MAX_ROWS; rows * max(in, out) and in * out are at most 2^32. */
+typedef struct {
+  int64_t rows;             /* product of the leading dimensions; 0 is allowed */
+  int64_t in;               /* columns of x, rows of the weights */
+  int64_t out;              /* columns of the weights */
+  int64_t x_stride;         /* elements between rows of x (0: in) */
+  int64_t weight_stride;    /* elements between rows of every weight (0: out), so that a weight may be a
+                               range of the columns of a wider, merged one */
+  int64_t residual_stride;  /* elements between rows of residual (0: out); hclrmix_linear only, otherwise 0 */
+  int32_t dtype;            /* hclrmix_dtype */
+  int32_t activation;       /* hclrmix_activation */
+  int32_t reserved[2];      /* must be 0 */
+} hclrmix_product;
+
+#define HCLRMIX_PRODUCT_MAX_WIDTH (1 << 21)
+
+/* y = residual + act(x @ weight + bias), with y [rows, out], bias [out] or
+ * NULL, residual [rows, out] or NULL. preact [rows, out] or NULL receives
+ * x @ weight + bias, which the backward pass of an activation takes. */
+hclrmix_status hclrmix_linear(const void* x, const void* weight, const void* bias, const void* residual, void* y,
+                              void* preact, void* workspace, size_t workspace_bytes, const hclrmix_product* problem,
+                              void* stream);
+
+/* Gradients of hclrmix_linear: with dz = dy * act'(preact) (dz = dy for
+ * ACT_NONE, where preact must be NULL), dx = dz @ weight^T [rows, in],
+ * d_weight = x^T @ dz [in, out], d_bias = sums of dz over the rows [out];
+ * each NULL when not wanted, at least one wanted (weight may be NULL without
+ * dx, x without d_weight). residual's gradient is dy itself. The two
+ * products take dz rounded to T, d_bias takes it before that rounding. With
+ * rows == 0, d_weight and d_bias are zeros. */
+hclrmix_status hclrmix_linear_backward(const void* x, const void* weight, const void* preact, const void* dy, void* dx,
+                                       void* d_weight, void* d_bias, void* workspace, size_t workspace_bytes,
+                                       const hclrmix_product* problem, void* stream);
+
+/* Gated feed-forward product: h = act(g) * u with g = x @ gate_weight +
+ * gate_bias and u = x @ up_weight + up_bias, in one kernel. h [rows, out];
+ * the biases [out], each or both NULL; g_out and u_out [rows, out], both NULL
+ * or both set, receive g and u for the backward pass. activation must not be
+ * ACT_NONE. */
+hclrmix_status hclrmix_glu(const void* x, const void* gate_weight, const void* up_weight, const void* gate_bias,
+                           const void* up_bias, void* h, void* g_out, void* u_out, void* workspace,
+                           size_t workspace_bytes, const hclrmix_product* problem, void* stream);
+
+/* Gradients of hclrmix_glu from its saved g and u: with dg = dh * u * act'(g)
+ * and du = dh * act(g),
+ *   dx = dg @ gate_weight^T + du @ up_weight^T,
+ *   d_gate_weight = x^T @ dg, d_up_weight = x^T @ du,
+ *   d_gate_bias, d_up_bias = sums of dg and du over the rows.
+ * Each output may be NULL when not wanted, but the two weights' gradients
+ * only together, and the two biases' likewise; at least one wanted (the
+ * weights may be NULL without dx, x without the weights' gradients). The
+ * products take dg and du rounded to T, the bias sums before that rounding.
+ * With rows == 0, the weights' and biases' gradients are zeros. */
+hclrmix_status hclrmix_glu_backward(const void* x, const void* gate_weight, const void* up_weight, const void* g,
+                                    const void* u, const void* dh, void* dx, void* d_gate_weight, void* d_up_weight,
+                                    void* d_gate_bias, void* d_up_bias, void* workspace, size_t workspace_bytes,
+                                    const hclrmix_product* problem, void* stream);
+
+/* Workspace of each product call, for any choice of its optional tensors and
+ * any strides. Every one is at least HCLRMIX_COUNTER_BYTES. */
+#define HCLRMIX_COUNTER_BYTES 4096
+hclrmix_status hclrmix_linear_workspace_size(const hclrmix_product* problem, size_t* bytes);
+hclrmix_status hclrmix_linear_backward_workspace_size(const hclrmix_product* problem, size_t* bytes);
+hclrmix_status hclrmix_glu_workspace_size(const hclrmix_product* problem, size_t* bytes);
+hclrmix_status hclrmix_glu_backward_workspace_size(const hclrmix_product* problem, size_t* bytes);
+
 /* Static description of a status code. */
 const char* hclrmix_status_string(hclrmix_status status);
 
