@@ -45,9 +45,11 @@ struct Gemm {
   void* out[2];
   void* save[2];
   int act, segments;
-  int tiles_m, tiles_n, splits;
+  int tiles_m, tiles_n;
+  int whole;        // tiles taken by one workgroup each (the first ones); the rest are split
+  int splits;       // parts of a split tile
   int vec4;         // four consecutive columns of every [M, N] tensor and bias are 4-element aligned
-  float* partial;   // [tile][split][BM * BN] fp32 (splits > 1)
+  float* partial;   // [split tile][split][BM * BN] fp32
   unsigned* counters;
 };
 
@@ -178,8 +180,9 @@ __device__ __forceinline__ void finish4(const Gemm& a, int b, int64_t m, int n, 
       st4<D>(a.save[0], i, left, a.vec4, v);
       st4<D>(a.save[1], i, left, a.vec4, u);
     }
+    act_n<D, 4>(a.act, v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = act_f(a.act, v[e]) * u[e];
+    for (int e = 0; e < 4; ++e) v[e] = v[e] * u[e];
     st4<D>(a.out[0], i, left, a.vec4, v);
   } else {
     if (a.bias[0]) {
@@ -188,10 +191,7 @@ __device__ __forceinline__ void finish4(const Gemm& a, int b, int64_t m, int n, 
       for (int e = 0; e < 4; ++e) v[e] = v[e] + t[e];
     }
     if (a.save[0]) st4<D>(a.save[0], i, left, a.vec4, v);
-    if (a.act != ACT_NONE) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = act_f(a.act, v[e]);
-    }
+    act_n<D, 4>(a.act, v);
     if (a.residual) {
       ld4<D>(a.residual, m * a.ldr + n, left, a.vec4, t);
 #pragma unroll
@@ -246,21 +246,34 @@ __device__ __forceinline__ bool join_splits(const Gemm& a, int tile, int split, 
 // that workgroups running together share the operands' tiles in its L2: groups of
 // eight tile rows, tile rows fastest, then tile columns.
 struct Place {
-  int b, tm, tn, split, tile;
+  int b, tm, tn;
+  int splits, split;  // parts of this tile (1: whole) and which one this is
+  int slot;           // index among the split tiles
 };
-__device__ __forceinline__ Place place(const Gemm& a) {
-  const int total = gridDim.x, id = blockIdx.x;
+__device__ __forceinline__ int xcd_order(int id, int total) {
   const int xcd = id & 7, per = total >> 3, rem = total & 7;
-  int w = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
+  return xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
+}
+__device__ __forceinline__ Place place(const Gemm& a) {
+  const int id = blockIdx.x;
   Place r;
-  r.split = w % a.splits;
-  w /= a.splits;
+  int tile;
+  if (id < a.whole) {
+    tile = xcd_order(id, a.whole);
+    r.splits = 1;
+    r.split = r.slot = 0;
+  } else {
+    const int w = xcd_order(id - a.whole, (int)gridDim.x - a.whole);
+    r.splits = a.splits;
+    r.slot = w / a.splits;
+    r.split = w - r.slot * a.splits;
+    tile = a.whole + r.slot;
+  }
   const int tiles = a.tiles_m * a.tiles_n;
-  r.tile = w;
-  r.b = w / tiles;
-  w -= r.b * tiles;
+  r.b = tile / tiles;
+  tile -= r.b * tiles;
   constexpr int GM = 8;
-  const int per_group = GM * a.tiles_n, group = w / per_group, in = w - group * per_group;
+  const int per_group = GM * a.tiles_n, group = tile / per_group, in = tile - group * per_group;
   const int rows = min(GM, a.tiles_m - group * GM);
   r.tm = group * GM + in % rows;
   r.tn = in / rows;
@@ -290,7 +303,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(const Gemm a) {
   for (int i = 0; i < FM * FN; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   const int kt = (a.K + BK - 1) / BK, steps = kt * a.segments;
-  const int t0 = (int)((int64_t)steps * pl.split / a.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / a.splits);
+  const int t0 = (int)((int64_t)steps * pl.split / pl.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / pl.splits);
   uint4 vp[TP::NI], vq[NQ][TQ::NI];
   auto fetch = [&](int t) {
     const int seg = t >= kt, k0 = (t - seg * kt) * BK, b = seg + pl.b;
@@ -321,10 +334,327 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product(const Gemm a) {
     }
   }
 
-  if (a.splits > 1 && !join_splits<FM * FN, THREADS>(a, pl.tile, pl.split, acc, tid)) return;
+  if (pl.splits > 1 && !join_splits<FM * FN, THREADS>(a, pl.slot, pl.split, acc, tid)) return;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int64_t m = m0 + (wm * FM + i) * 16 + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const int n = n0 + (wn * FQ + j) * 16 + 4 * (lane >> 4);
+      float v[4], u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = acc[i * FN + j][e];
+        if constexpr (DUAL) u[e] = acc[i * FN + FQ + j][e];
+      }
+      finish4<D, DUAL>(a, pl.b, m, n, v, u);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ 16-bit kernel, direct staging
+
+// Stages a tile by loads that write LDS themselves: no registers and no LDS
+// write instructions. One instruction per wave fills 1 KB of consecutive LDS,
+// so the chunk permutation is applied to the addresses instead. Loads go
+// through a buffer descriptor of the tile; lanes whose chunk lies outside the
+// operand get an offset beyond it, for which the load writes zeros.
+constexpr uint32_t OUTSIDE = 0x80000000u;
+__device__ __forceinline__ u32x4 raw_desc(const void* base) {
+  const uint64_t b = (uint64_t)base;
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)), 0x7FFFFFF0u, 0x00020000u};
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(const lds_u8*)p; }
+// Lane l: 16 bytes from offset off of the descriptor to LDS byte dst + 16 l (dst the
+// same in every lane). Written out because the compiler, which cannot tell the stage
+// being filled from the one being read, would wait for the load before every LDS read.
+__device__ __forceinline__ void lds_load16(u32x4 desc, uint32_t off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               : : "s"(dst), "v"(off), "s"(desc) : "memory");
+}
+
+// Where an operand's next tile starts and how many contraction indices it has from
+// there in its segment; steps go through the first segment, then the second.
+template <bool TR, int BK> struct Cursor {
+  const char* p;
+  const char* p1;  // the second segment's start
+  int64_t step;    // bytes from one tile to the next
+  int k, k1;
+  __device__ __forceinline__ void init(const void* q0, const void* q1, int64_t ld, int64_t r0, int K, int segments, int t,
+                                       int steps) {
+    const int64_t first = 2 * (TR ? r0 : r0 * ld);
+    step = 2 * (TR ? BK * ld : (int64_t)BK);
+    const int kt = (K + BK - 1) / BK;
+    p = (const char*)q0 + first;
+    p1 = (const char*)q1 + first;
+    k = K;
+    k1 = segments == 2 ? K : 0;
+    if (t >= kt) {
+      p = p1;
+      k1 = 0;
+      t -= kt;
+    }
+    p += t * step;
+    k -= t * BK;
+    // A split's range may end before its segments do.
+    stop = steps;
+  }
+  int stop;  // tiles left to load
+  __device__ __forceinline__ void next() {
+    p += step;
+    k -= BK;
+    --stop;
+    const bool turn = k <= 0;
+    p = turn ? p1 : p;
+    k = turn ? k1 : k;
+    k1 = turn ? 0 : k1;
+    k = stop > 0 ? k : 0;
+  }
+};
+
+template <bool TR, int R, int BK, int THREADS> struct Direct {
+  typedef Tile<DT::BF16, TR, R, BK, THREADS> T;
+  static constexpr int NI = T::NI;
+  static_assert(THREADS / T::CPR % 16 == 0 || NI == 1, "every chunk of a thread has the same place in its row");
+  uint32_t off[NI];  // byte offset of this lane's chunks from the tile's first element
+  int kk;            // contraction index of chunk 0 inside the tile
+  __device__ __forceinline__ void init(int64_t ld, int64_t r0, int64_t nr, int tid) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int c = i * THREADS + tid, row = c / T::CPR, ch = swz<TR, T::CPR>(row, c % T::CPR);
+      const bool in = TR ? r0 + 8 * ch < nr : r0 + row < nr;
+      off[i] = in ? (uint32_t)(row * (int)ld + 8 * ch) * 2u : OUTSIDE;
+    }
+    kk = TR ? tid / T::CPR : 8 * swz<TR, T::CPR>(tid / T::CPR, tid % T::CPR);
+  }
+  // The tile at p, k contraction indices of which exist, into LDS from byte address lds on
+  // (this wave's part).
+  __device__ __forceinline__ void stage(const char* p, int k, uint32_t lds, int wave) const {
+    const u32x4 r = raw_desc(p);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t o = kk + (TR ? i * (THREADS / T::CPR) : 0) < k ? off[i] : OUTSIDE;
+      lds_load16(r, o, __builtin_amdgcn_readfirstlane(lds + (i * THREADS + wave * 64) * 16));
+    }
+  }
+};
+
+// Waits until at most N of this wave's loads are in flight (they complete in order).
+template <int N> __device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// All of this wave's LDS reads are done and its direct loads have arrived; then all waves'.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <DT D, bool PT, bool QT, bool DUAL, int BM, int BN, int BK, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void k_product_direct(const Gemm a) {
+  constexpr int THREADS = 64 * WM * WN, NQ = DUAL ? 2 : 1;
+  constexpr int FM = BM / WM / 16, FN = BN / WN / 16, FQ = FN / NQ;
+  typedef Tile<D, PT, BM, BK, THREADS> TP;
+  typedef Tile<D, QT, BN / NQ, BK, THREADS> TQ;
+  constexpr int STAGE = TP::BYTES + NQ * TQ::BYTES;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / WN, wn = wave % WN;
+  const Place pl = place(a);
+  const int64_t m0 = (int64_t)pl.tm * BM;
+  const int n0 = pl.tn * (BN / NQ);
+
+  f32x4 acc[FM * FN];
+#pragma unroll
+  for (int i = 0; i < FM * FN; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const int kt = (a.K + BK - 1) / BK, steps = kt * a.segments;
+  const int t0 = (int)((int64_t)steps * pl.split / pl.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / pl.splits);
+  Direct<PT, BM, BK, THREADS> dp;
+  Direct<QT, BN / NQ, BK, THREADS> dq;
+  dp.init(a.ldp, m0, a.M, tid);
+  dq.init(a.ldq, n0, a.N, tid);
+  Cursor<PT, BK> cp;
+  Cursor<QT, BK> cq[NQ];
+  cp.init(a.p[pl.b], a.p[1], a.ldp, m0, a.K, a.segments, t0, t1 - t0);
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) cq[i].init(a.q[pl.b + i], a.q[1], a.ldq, n0, a.K, a.segments, t0, t1 - t0);
+  const uint32_t l0 = lds_offset(lds);
+  const int w = __builtin_amdgcn_readfirstlane(wave);
+  auto stage = [&](int buf) {
+    const uint32_t to = l0 + buf * STAGE;
+    dp.stage(cp.p, cp.k, to, w);
+    cp.next();
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      dq.stage(cq[i].p, cq[i].k, to + TP::BYTES + i * TQ::BYTES, w);
+      cq[i].next();
+    }
+  };
+  stage(0);
+  for (int t = t0; t < t1; ++t) {
+    const unsigned char* cur = lds + ((t - t0) & 1) * STAGE;
+    const unsigned char* curq = cur + TP::BYTES;
+    stage_barrier();
+    if (t + 1 < t1) stage((t + 1 - t0) & 1);
+#pragma unroll
+    for (int k = 0; k < BK; k += 32) {
+      s16x8 fp[FM], fq[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fq[j] = TQ::frag(curq + (j / FQ) * TQ::BYTES, (wn * FQ + j % FQ) * 16, k, lane);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fp[i] = TP::frag(cur, (wm * FM + i) * 16, k, lane);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i * FN + j] = mfma<D>(fq[j], fp[i], acc[i * FN + j]);
+    }
+  }
+
+  if (pl.splits > 1 && !join_splits<FM * FN, THREADS>(a, pl.slot, pl.split, acc, tid)) return;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + (wm * FM + i) * 16 + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const int n = n0 + (wn * FQ + j) * 16 + 4 * (lane >> 4);
+      float v[4], u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = acc[i * FN + j][e];
+        if constexpr (DUAL) u[e] = acc[i * FN + FQ + j][e];
+      }
+      finish4<D, DUAL>(a, pl.b, m, n, v, u);
+    }
+  }
+}
+
+// 256 x 256 tile, contraction steps of 64, eight waves, for products with many tiles. Wave
+// (wm, wn) owns 64 rows of each half of the tile's rows and 64 columns (dual: 32 of g, the
+// same 32 of u). A step has two phases of 32 matrix ops per wave: phase 0 reads all of the
+// wave's Q fragments, which stay in registers, and its P fragments of the first half; phase
+// 1 those of the second half. So Q and the first half of P are free for the loads of step
+// t + 2 one phase after they arrived, and every load has three phases to arrive in two
+// buffers.
+// Two waves share each SIMD (w and w + 4) and run half a phase apart: while one reads its
+// fragments, the other's matrix ops run. Barriers split time into intervals: waves 0..3 read
+// for phase j in interval 2j and compute in 2j + 1, waves 4..7 in 2j + 1 and 2j + 2. A wave
+// has its fragments (lgkmcnt 0) before it leaves a reading interval, so a buffer read for
+// phase j is free from interval 2j + 2 on, when the first loads into it are issued; and every
+// wave waits for its own loads of phase j + 1 by the end of interval 2j + 1, one interval before
+// they are first read. Loads past the last step write zeros into free buffers, so that the
+// number of loads in flight is the same in every phase.
+template <DT D, bool PT, bool QT, bool DUAL>
+__global__ __launch_bounds__(512) void k_product_wide(const Gemm a) {
+  constexpr int THREADS = 512, NQ = DUAL ? 2 : 1, BK = 64, FM = 8, FN = 4, FQ = FN / NQ;
+  typedef Tile<D, PT, 128, BK, THREADS> TP;
+  typedef Tile<D, QT, 256 / NQ, BK, THREADS> TQ;
+  constexpr int QBYTES = NQ * TQ::BYTES, STAGE = QBYTES + 2 * TP::BYTES;
+  constexpr int LQ = NQ * TQ::NI, LP = TP::NI;  // loads of a wave for Q, and for half of P
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 2, wn = wave & 3;
+  const Place pl = place(a);
+  const int64_t m0 = (int64_t)pl.tm * 256;
+  const int n0 = pl.tn * (256 / NQ);
+
+  f32x4 acc[FM * FN];
+#pragma unroll
+  for (int i = 0; i < FM * FN; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const int kt = (a.K + BK - 1) / BK, steps = kt * a.segments;
+  const int t0 = (int)((int64_t)steps * pl.split / pl.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / pl.splits);
+  Direct<PT, 128, BK, THREADS> dp[2];
+  Direct<QT, 256 / NQ, BK, THREADS> dq;
+  dp[0].init(a.ldp, m0, a.M, tid);
+  dp[1].init(a.ldp, m0 + 128, a.M, tid);
+  dq.init(a.ldq, n0, a.N, tid);
+  Cursor<PT, BK> cp[2];
+  Cursor<QT, BK> cq[NQ];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) cp[h].init(a.p[pl.b], a.p[1], a.ldp, m0 + 128 * h, a.K, a.segments, t0, t1 - t0);
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) cq[i].init(a.q[pl.b + i], a.q[1], a.ldq, n0, a.K, a.segments, t0, t1 - t0);
+  const uint32_t l0 = lds_offset(lds);
+  const int w = __builtin_amdgcn_readfirstlane(wave);
+  auto load_q = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      dq.stage(cq[i].p, cq[i].k, l0 + buf * STAGE + i * TQ::BYTES, w);
+      cq[i].next();
+    }
+  };
+  auto load_p = [&](int buf, int h) {
+    dp[h].stage(cp[h].p, cp[h].k, l0 + buf * STAGE + QBYTES + h * TP::BYTES, w);
+    cp[h].next();
+  };
+  load_q(0);
+  load_p(0, 0);
+  load_p(0, 1);
+  load_q(1);
+  load_p(1, 0);
+  load_p(1, 1);
+  wait_loads<LQ + 2 * LP>();
+  __builtin_amdgcn_s_barrier();
+  s16x8 fq[2][FN], fp[2][FM / 2];
+  const unsigned char* cur = lds;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fq[k][j] = TQ::frag(cur + (j / FQ) * TQ::BYTES, (wn * FQ + j % FQ) * 16, 32 * k, lane);
+#pragma unroll
+    for (int i = 0; i < FM / 2; ++i) fp[k][i] = TP::frag(cur + QBYTES, (wm * 4 + i) * 16, 32 * k, lane);
+  }
+  for (int t = t0; t < t1; ++t) {
+    const int buf = (t - t0) & 1;
+    const unsigned char* next = lds + (buf ^ 1) * STAGE;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const unsigned char* np = half == 0 ? cur + QBYTES + TP::BYTES : next + QBYTES;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < FM / 2; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            f32x4& c = acc[(half * FM / 2 + i) * FN + j];
+            c = mfma<D>(fq[k][j], fp[k][i], c);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          fp[k][i] = TP::frag(np, (wm * 4 + i) * 16, 32 * k, lane);
+          if (half == 1 && i == FM / 2 - 1) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              fq[k][j] = TQ::frag(next + (j / FQ) * TQ::BYTES, (wn * FQ + j % FQ) * 16, 32 * k, lane);
+          }
+          if (k == 0 && i == FM / 2 - 1) {
+            // Everything read before this phase has arrived (younger: this phase's fragments so far).
+            if (half == 0) wait_loads<LP>();
+            else wait_loads<LQ + LP>();
+            asm volatile("s_waitcnt lgkmcnt(%0)" : : "n"(min(15, half == 0 ? (PT ? 8 : 4) : (PT ? 8 : 4) + (QT ? 8 : 4))) : "memory");
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            if (half == 0) {
+              load_q(buf);
+              load_p(buf, 0);
+            } else {
+              load_p(buf, 1);
+            }
+          }
+        }
+      }
+    }
+    cur = next;
+  }
+  wait_loads<0>();  // LDS must not be given up with loads into it in flight
+
+  if (pl.splits > 1 && !join_splits<FM * FN, THREADS>(a, pl.slot, pl.split, acc, tid)) return;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + (i / 4) * 128 + (wm * 4 + i % 4) * 16 + (lane & 15);
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
       const int n = n0 + (wn * FQ + j) * 16 + 4 * (lane >> 4);
@@ -414,7 +744,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product32(const Gemm a, const 
 #pragma unroll
   for (int i = 0; i < NA; ++i) acc[i] = tot[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int kt = (a.K + BK - 1) / BK, steps = kt * a.segments;
-  const int t0 = (int)((int64_t)steps * pl.split / a.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / a.splits);
+  const int t0 = (int)((int64_t)steps * pl.split / pl.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / pl.splits);
   f32x4 vp[TP::NI], vq[NQ][TQ::NI];
   auto fetch = [&](int t) {
     const int seg = t >= kt, k0 = (t - seg * kt) * BK, b = seg + pl.b;
@@ -453,7 +783,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product32(const Gemm a, const 
 #pragma unroll
   for (int i = 0; i < NA; ++i) acc[i] = tot[i] + acc[i];
 
-  if (a.splits > 1 && !join_splits<NA, THREADS>(a, pl.tile, pl.split, acc, tid)) return;
+  if (pl.splits > 1 && !join_splits<NA, THREADS>(a, pl.slot, pl.split, acc, tid)) return;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int64_t m = m0 + (wm * FM + i) * 16 + (lane & 15);
@@ -476,31 +806,81 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product32(const Gemm a, const 
 // Tile shape and split of a product.
 struct Plan {
   int bm, bn, bk;
-  int tiles_m, tiles_n, splits;
+  int tiles_m, tiles_n;
+  int64_t whole, rest;  // tiles taken whole, and split
+  int splits;           // parts of each split tile
+  double us;            // what the model below expects
 };
 
-static Plan make_plan(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch) {
-  Plan p;
-  const bool few = M <= 16 && !p_trans;
-  p.bm = few ? 16 : 128;
-  p.bn = few && !dual ? 64 : 128;
-  p.bk = dtype == HCLRMIX_F32 ? 16 : (few ? 128 : 64);
+// A shape's tiles run in rounds of `slots` workgroups. Full rounds take their tiles whole; the
+// tiles left over (all of them, where there are fewer than slots) are split along the
+// contraction where that ends sooner: parts run shorter, the last one to arrive reads
+// `splits` fp32 tiles. Times in microseconds, fitted to measurements.
+struct Shape {
+  int bm, bn, bk, slots;
+  double step, fixed, join;  // of one round: per contraction step, per tile, per part joined
+};
+
+static Plan shape_plan(const Shape& sh, int64_t M, int64_t N, int64_t K, bool dual, int segments, int batch) {
+  Plan p{};
+  p.bm = sh.bm;
+  p.bn = sh.bn;
+  p.bk = sh.bk;
   const int cols = dual ? p.bn / 2 : p.bn;
   p.tiles_m = (int)((M + p.bm - 1) / p.bm);
   p.tiles_n = (int)((N + cols - 1) / cols);
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * batch;
   const int64_t steps = (K + p.bk - 1) / p.bk * segments;
-  int64_t s = 1;
-  if (tiles <= MAX_SPLIT_TILES && tiles < 384) s = std::min<int64_t>(768 / tiles, steps / (few ? 2 : 4));
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, 64));
+  const int64_t rounds = tiles / sh.slots, rest = tiles % sh.slots;
+  const double one = steps * sh.step + sh.fixed;
+  int splits = 1;
+  double best = rest ? one : 0.0;
+  if (rest && rest <= MAX_SPLIT_TILES) {
+    for (int s = 2; s <= 64 && s * 2 <= steps; ++s) {
+      if (rest * s > 4 * sh.slots) break;
+      const double parts = (double)((rest * s + sh.slots - 1) / sh.slots);
+      const double t = parts * ((double)((steps + s - 1) / s) * sh.step + sh.fixed) + (s + 2) * sh.join;
+      if (t < best) {
+        best = t;
+        splits = s;
+      }
+    }
+  }
+  p.splits = splits;
+  p.rest = splits > 1 ? rest : 0;
+  p.whole = tiles - p.rest;
+  p.us = rounds * one + best;
   return p;
 }
 
+constexpr Shape WIDE{256, 256, 64, 256, 1.70, 6.0, 2.0};
+constexpr Shape MID{128, 128, 64, 512, 1.06, 4.0, 0.6};
+constexpr Shape FEW{16, 64, 128, 768, 0.6, 3.0, 0.1};
+constexpr Shape FEW_DUAL{16, 128, 128, 768, 1.2, 3.0, 0.2};
+constexpr Shape MID32{128, 128, 16, 512, 3.0, 4.0, 0.6};
+constexpr Shape FEW32{16, 64, 16, 768, 0.2, 3.0, 0.1};
+constexpr Shape FEW32_DUAL{16, 128, 16, 768, 0.4, 3.0, 0.2};
+
+static Plan make_plan(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch,
+                      bool aln) {
+  auto plan = [&](const Shape& s) { return shape_plan(s, M, N, K, dual, segments, batch); };
+  const bool f32 = dtype == HCLRMIX_F32;
+  if (M <= 16 && !p_trans) return plan(f32 ? (dual ? FEW32_DUAL : FEW32) : (dual ? FEW_DUAL : FEW));
+  if (f32) return plan(MID32);
+  const Plan mid = plan(MID);
+  if (!aln) return mid;
+  const Plan wide = plan(WIDE);
+  return wide.us < mid.us ? wide : mid;
+}
+
 size_t product_scratch(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch) {
-  if (M == 0) return 0;
-  const Plan p = make_plan(dtype, M, N, K, p_trans, dual, segments, batch);
-  if (p.splits == 1) return 0;
-  return (size_t)p.tiles_m * p.tiles_n * batch * p.splits * p.bm * p.bn * 4;
+  if (M == 0 || K == 0) return 0;
+  size_t most = 0;
+  for (int aln = 0; aln < 2; ++aln) {
+    const Plan p = make_plan(dtype, M, N, K, p_trans, dual, segments, batch, aln != 0);
+    most = std::max(most, (size_t)p.rest * p.splits * p.bm * p.bn * 4);
+  }
+  return most;
 }
 
 template <DT D, bool PT, bool QT, bool DUAL>
@@ -512,7 +892,9 @@ static hipError_t go16(const Gemm& g, const Plan& p, bool aln, unsigned grid, hi
                  : launch(nullptr, k_product<D, PT, QT, DUAL, 16, DUAL ? 128 : 64, 128, 1, 4, false>, dim3(grid), dim3(256),
                           0, s, g);
   }
-  return aln ? launch(nullptr, k_product<D, PT, QT, DUAL, 128, 128, 64, 2, 2, true>, dim3(grid), dim3(256), 0, s, g)
+  if (p.bm == 256)
+    return launch(nullptr, k_product_wide<D, PT, QT, DUAL>, dim3(grid), dim3(512), 0, s, g);
+  return aln ? launch(nullptr, k_product_direct<D, PT, QT, DUAL, 128, 128, 64, 2, 2>, dim3(grid), dim3(256), 0, s, g)
              : launch(nullptr, k_product<D, PT, QT, DUAL, 128, 128, 64, 2, 2, false>, dim3(grid), dim3(256), 0, s, g);
 }
 
@@ -534,7 +916,6 @@ static hipError_t go(const Gemm& g, const Plan& p, int dtype, bool aln, unsigned
 
 hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* counters, hipStream_t s) {
   if (p.M == 0) return hipSuccess;
-  const Plan pl = make_plan(dtype, p.M, p.N, p.K, p.p_trans, p.dual, p.segments, p.batch);
   Gemm g{};
   const uintptr_t es = dtype == HCLRMIX_F32 ? 4 : 2, a16 = 16 / es;
   // 16-byte accesses: rows start on them and their ends do too.
@@ -552,6 +933,7 @@ hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* 
     v4 = v4 && on(p.bias[i], 4 * es) && on(p.out[i], 4 * es) && on(p.save[i], 4 * es);
   }
   v4 = v4 && on(p.residual, 4 * es);
+  const Plan pl = make_plan(dtype, p.M, p.N, p.K, p.p_trans, p.dual, p.segments, p.batch, aln);
   g.ldp = p.ldp;
   g.ldq = p.ldq;
   g.ldr = p.ldr;
@@ -563,11 +945,12 @@ hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* 
   g.segments = p.segments;
   g.tiles_m = pl.tiles_m;
   g.tiles_n = pl.tiles_n;
+  g.whole = (int)pl.whole;
   g.splits = pl.splits;
   g.vec4 = v4;
   g.partial = (float*)scratch;
   g.counters = counters;
-  const int64_t grid = (int64_t)pl.tiles_m * pl.tiles_n * p.batch * pl.splits;
+  const int64_t grid = pl.whole + pl.rest * pl.splits;
   if (grid > 0x3FFFFF) return hipErrorInvalidValue;
   const unsigned n = (unsigned)grid;
   if (p.dual) return go<false, true, true>(g, pl, dtype, aln, n, s);
@@ -600,27 +983,30 @@ __global__ __launch_bounds__(256) void k_act_grad(const void* dy, const void* p,
   if (left > 0) {
     for (int64_t r = r0 + sub; r < r1; r += 4) {
       const int64_t i = r * cols + c;
-      float g[8], x[8], y[8], v[8];
+      float g[8], x[8], y[8], df[8];
       load8<D, ALN>(dy, i, left, g);
-      if (p) load8<D, ALN>(p, i, left, x);
-      if (GLU) load8<D, ALN>(u, i, left, y);
+      if (p) {
+        load8<D, ALN>(p, i, left, x);
+        act_slope_n<D, 8>(act, x, df);
+      }
+      if (GLU) {
+        load8<D, ALN>(u, i, left, y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float df = 1.0f, f = 0.0f;
-        if (p) f = act_df(act, x[e], df);
-        if (GLU) {
-          const float a = g[e] * y[e] * df, b = g[e] * f;
-          s0[e] = s0[e] + a;
-          s1[e] = s1[e] + b;
-          g[e] = a;
-          v[e] = b;
-        } else {
-          g[e] = g[e] * df;
+        for (int e = 0; e < 8; ++e) {
+          x[e] = g[e] * x[e];
+          g[e] = g[e] * y[e] * df[e];
+          s0[e] = s0[e] + g[e];
+          s1[e] = s1[e] + x[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (p) g[e] = g[e] * df[e];
           s0[e] = s0[e] + g[e];
         }
       }
       if (d0) store8<D, ALN>(d0, i, left, g);
-      if (GLU && d1) store8<D, ALN>(d1, i, left, v);
+      if (GLU && d1) store8<D, ALN>(d1, i, left, x);
     }
   }
   if (!partial) return;

@@ -248,6 +248,32 @@ def test_glu_backward(i, shape, dtype):
     same(out[:3], hc.glu_backward(x, wg, wu, g, u, dh, activation=act)[:3], "without biases")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_products_of_many_tiles(dtype):
+    """Enough output tiles for the 256 x 256 kernel in each operand layout,
+    with ragged edges, and left-over tiles whose contraction is split."""
+    dt = T_OF[dtype]
+    for m, k, n in ((4090, 1032, 4088), (4090, 2600, 4600)):
+        print(f"[many tiles] linear {m} {k} {n}", flush=True)
+        x, w, b, res = linear_inputs(m, k, n, dt, 11)
+        within(hc.linear(x, w, b, res, activation="silu"), *R.linear(x, w, b, res, "silu")[:2], ("linear", m, k, n))
+    m, k, n = 4090, 264, 2040
+    print(f"[many tiles] glu {m} {k} {n}", flush=True)
+    x, wg, bg, _ = linear_inputs(m, k, n, dt, 12)
+    _, wu, bu, _ = linear_inputs(m, k, n, dt, 13)
+    ref = R.glu(x, wg, wu, bg, bu, "gelu")
+    for got, name in zip(hc.glu(x, wg, wu, bg, bu, activation="gelu", save=True), ("h", "g", "u")):
+        within(got, *ref[name], (name, m, k, n))
+    for m, k, n in ((4090, 4088, 520), (520, 4088, 4088)):
+        print(f"[many tiles] glu_backward {m} {k} {n}", flush=True)
+        x, wg, _, _ = linear_inputs(m, k, n, dt, 14)
+        wu = rand((k, n), dt, 15, k ** -0.5)
+        g, u, dh = (rand((m, n), dt, s) for s in (3, 4, 5))
+        ref = R.glu_backward(x, wg, wu, g, u, dh, "silu")
+        for got, name in zip(hc.glu_backward(x, wg, wu, g, u, dh, bias=True), GLU_NAMES):
+            within(got, *ref[name], (name, m, k, n))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("m,k,n", [(3, 520, 96), (150, 264, 200), (150, 263, 201)])
 def test_strided_operands_and_unaligned_tensors(m, k, n, dtype):
