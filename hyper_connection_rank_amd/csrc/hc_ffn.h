@@ -173,6 +173,64 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, int n, float*
   }
 }
 
+// A buffer descriptor of `bytes` bytes from base (the same in every lane). Loads past its end
+// give zeros, stores there are dropped.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
+
+// Eight elements as they are stored (half the registers of their fp32 values for 16-bit T).
+// Aligned loads are non-temporal: rows are read once.
+template <DT D> struct Raw8 {
+  u32x4 v;
+};
+template <> struct Raw8<DT::F32> {
+  u32x4 v, w;
+};
+template <DT D, bool ALN> __device__ __forceinline__ Raw8<D> load_raw8(const void* base, int64_t i, int n) {
+  Raw8<D> r;
+  if constexpr (ALN) {
+    const u32x4* p = (const u32x4*)((const typename Store<D>::type*)base + i);
+    r.v = __builtin_nontemporal_load(p);
+    if constexpr (D == DT::F32) r.w = __builtin_nontemporal_load(p + 1);
+  } else if constexpr (D == DT::F32) {
+    float x[8];
+    load8<D, ALN>(base, i, n, x);
+    r.v = __builtin_bit_cast(u32x4, f32x4{x[0], x[1], x[2], x[3]});
+    r.w = __builtin_bit_cast(u32x4, f32x4{x[4], x[5], x[6], x[7]});
+  } else {
+    const uint16_t* p = (const uint16_t*)base + i;
+    if (n >= 8) {
+      r.v = to_u32x4(ld16<D, ALN>(p));
+    } else {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < n) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+      r.v = u32x4{w[0], w[1], w[2], w[3]};
+    }
+  }
+  return r;
+}
+template <DT D> __device__ __forceinline__ Raw8<D> zero_raw8() {
+  Raw8<D> r;
+  r.v = u32x4{0u, 0u, 0u, 0u};
+  if constexpr (D == DT::F32) r.w = r.v;
+  return r;
+}
+template <DT D> __device__ __forceinline__ void unpack_raw8(const Raw8<D>& r, float* x) {
+  if constexpr (D == DT::F32) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = __uint_as_float(r.v[e]);
+      x[4 + e] = __uint_as_float(r.w[e]);
+    }
+  } else {
+    unpack8<D>(to_uint4(r.v), x);
+  }
+}
+
 // Rounds eight values to T and stores the first n.
 template <DT D, bool ALN>
 __device__ __forceinline__ void store8(void* base, int64_t i, int n, const float* x) {
@@ -205,7 +263,8 @@ struct NormArgs {
   const void *dres, *dn;                    // backward: gradients of residual_out and normed, or null
   void *res_out, *normed;                   // forward
   void *dy, *d_residual, *d_gate;           // backward, each or null
-  float* partial;                           // backward: [G][2][hidden] sums of the scales' gradients, or null
+  void *d_post, *d_pre;                     // backward: the scales' gradients, each or null
+  float* partial;                           // backward: [groups][2][hidden] sums of the scales' gradients
   int64_t rows, gate_stride;
   int hidden, gate_kind, post_norm;
   float alpha, eps;
@@ -213,12 +272,11 @@ struct NormArgs {
 
 hipError_t launch_norm(const NormArgs& a, int dtype, bool aligned, hipStream_t s);
 // Workgroups of the backward kernel, each with one row of partial sums.
-int norm_backward_groups(int64_t rows);
-hipError_t launch_norm_backward(const NormArgs& a, int dtype, bool aligned, int groups, hipStream_t s);
+int norm_backward_groups(int64_t rows, int64_t hidden);
+hipError_t launch_norm_backward(const NormArgs& a, int dtype, bool aligned, hipStream_t s);
 
-// out[b][c] = T(sum over r, ascending, of partial[r][b * cols + c]) for b < 2 with
-// out[b] not null; partial is [nrows][2 * cols] (or [nrows][cols] with out[1]
-// null and pitch = cols).
+// out0[c], out1[c] (each or null) = T(sum over r, in a fixed order, of partial[r * pitch + c]
+// and of partial[r * pitch + cols + c]) for c < cols.
 hipError_t launch_column_sums(const float* partial, int nrows, int64_t pitch, int64_t cols, void* out0, void* out1,
                               int dtype, hipStream_t s);
 
@@ -251,13 +309,13 @@ size_t product_scratch(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans,
 // scratch: product_scratch() bytes; counters: HCLRMIX_COUNTER_BYTES, zero.
 hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* counters, hipStream_t s);
 
-// dz = dy * act'(p) [rows, cols], and per-group column sums of dz before its
-// rounding into partial [G][cols] (G = grad_groups(rows); null: not wanted).
-// Glu form (u not null): d0 = dy * u * act'(p), d1 = dy * act(p), partial
-// [G][2 * cols]. d0 and d1 may be null (only sums wanted).
+// dz = dy * act'(p) [rows, cols] into d0 and, with partial not null, the column sums of dz
+// before its rounding into b0 [cols] (partial: grad_groups(rows) rows of scratch). Glu form
+// (u not null): d0 = dy * u * act'(p), d1 = dy * act(p), sums into b0 and b1, scratch rows of
+// 2 * cols. d0 and d1 may be null (only sums wanted).
 int grad_groups(int64_t rows);
-hipError_t launch_act_grad(const void* dy, const void* p, const void* u, void* d0, void* d1, float* partial,
-                           int64_t rows, int64_t cols, int act, int dtype, bool aligned, hipStream_t s);
+hipError_t launch_act_grad(const void* dy, const void* p, const void* u, void* d0, void* d1, float* partial, void* b0,
+                           void* b1, int64_t rows, int64_t cols, int act, int dtype, bool aligned, hipStream_t s);
 
 // Writes zeros (n bytes, a multiple of 2).
 hipError_t launch_zero(void* p, size_t n, hipStream_t s);

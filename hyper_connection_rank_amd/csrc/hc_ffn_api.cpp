@@ -105,7 +105,7 @@ Range gate_span(const char* name, const void* gate, const hclrmix_norm_problem* 
 }
 
 size_t norm_workspace(const hclrmix_norm_problem* p) {
-  return HCLRMIX_COUNTER_BYTES + up256((size_t)hc::norm_backward_groups(p->rows) * 2 * (size_t)p->hidden * 4);
+  return HCLRMIX_COUNTER_BYTES + up256((size_t)hc::norm_backward_groups(p->rows, p->hidden) * 2 * (size_t)p->hidden * 4);
 }
 
 // ------------------------------------------------------------------ products
@@ -321,14 +321,13 @@ hclrmix_status hclrmix_residual_norm_backward(const void* y, const void* residua
   a.dy = dy;
   a.d_residual = d_residual;
   a.d_gate = d_gate;
+  a.d_post = d_post_scale;
+  a.d_pre = d_pre_scale;
   a.partial = sums ? (float*)((char*)workspace + HCLRMIX_COUNTER_BYTES) : nullptr;
   const bool aln = h % 8 == 0 && all16({y, residual_out, p.gate == HCLRMIX_GATE_ELEMENT ? gate : nullptr,
                                         p.gate == HCLRMIX_GATE_ELEMENT ? d_gate : nullptr, post_scale, pre_scale,
-                                        d_residual_out, d_normed, dy, d_residual});
-  const int groups = hc::norm_backward_groups(m);
-  hipError_t e = hc::launch_norm_backward(a, p.dtype, aln, groups, s);
-  if (e == hipSuccess && sums) e = hc::launch_column_sums(a.partial, groups, 2 * h, h, d_post_scale, d_pre_scale, p.dtype, s);
-  return done(e);
+                                        d_residual_out, d_normed, dy, d_residual, d_post_scale, d_pre_scale});
+  return done(hc::launch_norm_backward(a, p.dtype, aln, s));
 }
 
 hclrmix_status hclrmix_linear(const void* x, const void* weight, const void* bias, const void* residual, void* y,
@@ -449,9 +448,8 @@ hclrmix_status hclrmix_linear_backward(const void* x, const void* weight, const 
   void* dz = act && products ? ws + w.dz0 : nullptr;
   float* sums = d_bias ? (float*)(ws + w.sums) : nullptr;
   if (dz || sums)
-    e = hc::launch_act_grad(dy, preact, nullptr, dz, nullptr, sums, m, n, p.activation, p.dtype,
+    e = hc::launch_act_grad(dy, preact, nullptr, dz, nullptr, sums, d_bias, nullptr, m, n, p.activation, p.dtype,
                             n % 8 == 0 && all16({dy, preact}), s);
-  if (e == hipSuccess && d_bias) e = hc::launch_column_sums(sums, hc::grad_groups(m), n, n, d_bias, nullptr, p.dtype, s);
   const void* d = act ? dz : dy;
   if (e == hipSuccess && dx)
     e = hc::launch_product(dx_product(problem, st_, d, nullptr, weight, nullptr, dx), p.dtype, ws + w.scratch, (unsigned*)ws, s);
@@ -502,9 +500,8 @@ hclrmix_status hclrmix_glu_backward(const void* x, const void* gate_weight, cons
   void* dg = products ? ws + w.dz0 : nullptr;
   void* du = products ? ws + w.dz1 : nullptr;
   float* sums = d_gate_bias ? (float*)(ws + w.sums) : nullptr;
-  e = hc::launch_act_grad(dh, g, u, dg, du, sums, m, n, p.activation, p.dtype, n % 8 == 0 && all16({dh, g, u}), s);
-  if (e == hipSuccess && sums)
-    e = hc::launch_column_sums(sums, hc::grad_groups(m), 2 * n, n, d_gate_bias, d_up_bias, p.dtype, s);
+  e = hc::launch_act_grad(dh, g, u, dg, du, sums, d_gate_bias, d_up_bias, m, n, p.activation, p.dtype,
+                          n % 8 == 0 && all16({dh, g, u}), s);
   if (e == hipSuccess && dx)
     e = hc::launch_product(dx_product(problem, st_, dg, du, gate_weight, up_weight, dx), p.dtype, ws + w.scratch, (unsigned*)ws, s);
   if (e == hipSuccess && d_gate_weight)

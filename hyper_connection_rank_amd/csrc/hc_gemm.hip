@@ -201,10 +201,6 @@ __device__ __forceinline__ void finish4(const Gemm& a, int b, int64_t m, int n, 
   }
 }
 
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
-}
 constexpr uint32_t OUTSIDE = 0x80000000u;  // an offset past every descriptor's end: loads give zeros, stores nothing
 constexpr int AGENT = 16;  // sc1: the access is coherent across the chip's L2s
 
@@ -1044,7 +1040,7 @@ hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* 
 
 // ------------------------------------------------------------------ activation gradients
 
-constexpr int GRAD_ROWS = 32;  // rows per group, at least
+constexpr int GRAD_ROWS = 64;  // rows per group, at least
 
 int grad_groups(int64_t rows) {
   const int64_t g = (rows + GRAD_ROWS - 1) / GRAD_ROWS;
@@ -1052,10 +1048,11 @@ int grad_groups(int64_t rows) {
 }
 
 // A thread takes eight columns of its group's rows (a contiguous range),
-// ascending, and holds their column sums.
+// ascending, and holds their column sums. With one group the sums are the
+// bias gradients themselves (b0, b1); otherwise they go to partial.
 template <DT D, bool ALN, bool GLU>
 __global__ __launch_bounds__(256) void k_act_grad(const void* dy, const void* p, const void* u, void* d0, void* d1,
-                                                  float* partial, int64_t rows, int64_t cols, int act) {
+                                                  float* partial, void* b0, void* b1, int64_t rows, int64_t cols, int act) {
   const int64_t c = ((int64_t)blockIdx.x * 64 + (threadIdx.x & 63)) * 8;
   const int sub = threadIdx.x >> 6;
   __shared__ float red[4][64][9];
@@ -1102,32 +1099,36 @@ __global__ __launch_bounds__(256) void k_act_grad(const void* dy, const void* p,
     __syncthreads();
     for (int j = threadIdx.x; j < 512; j += 256) {
       const int64_t col = (int64_t)blockIdx.x * 512 + j;
-      if (col < cols)
-        partial[((int64_t)blockIdx.y * (GLU ? 2 : 1) + h) * cols + col] =
+      if (col < cols) {
+        const float sum =
             ((red[0][j >> 3][j & 7] + red[1][j >> 3][j & 7]) + red[2][j >> 3][j & 7]) + red[3][j >> 3][j & 7];
+        if (gridDim.y == 1) st<D>(h ? b1 : b0, col, sum);
+        else partial[((int64_t)blockIdx.y * (GLU ? 2 : 1) + h) * cols + col] = sum;
+      }
     }
   }
 }
 
 template <DT D, bool ALN>
-static hipError_t act_grad(const void* dy, const void* p, const void* u, void* d0, void* d1, float* partial,
-                           int64_t rows, int64_t cols, int act, hipStream_t s) {
+static hipError_t act_grad(const void* dy, const void* p, const void* u, void* d0, void* d1, float* partial, void* b0,
+                           void* b1, int64_t rows, int64_t cols, int act, hipStream_t s) {
   const dim3 grid((unsigned)((cols + 511) / 512), (unsigned)grad_groups(rows));
-  return u ? launch(nullptr, k_act_grad<D, ALN, true>, grid, dim3(256), 0, s, dy, p, u, d0, d1, partial, rows, cols, act)
-           : launch(nullptr, k_act_grad<D, ALN, false>, grid, dim3(256), 0, s, dy, p, u, d0, d1, partial, rows, cols, act);
+  return u ? launch(nullptr, k_act_grad<D, ALN, true>, grid, dim3(256), 0, s, dy, p, u, d0, d1, partial, b0, b1, rows, cols, act)
+           : launch(nullptr, k_act_grad<D, ALN, false>, grid, dim3(256), 0, s, dy, p, u, d0, d1, partial, b0, b1, rows, cols, act);
 }
 
-hipError_t launch_act_grad(const void* dy, const void* p, const void* u, void* d0, void* d1, float* partial,
-                           int64_t rows, int64_t cols, int act, int dtype, bool aligned, hipStream_t s) {
+hipError_t launch_act_grad(const void* dy, const void* p, const void* u, void* d0, void* d1, float* partial, void* b0,
+                           void* b1, int64_t rows, int64_t cols, int act, int dtype, bool aligned, hipStream_t s) {
   if (rows == 0) return hipSuccess;
-  if (dtype == HCLRMIX_BF16)
-    return aligned ? act_grad<DT::BF16, true>(dy, p, u, d0, d1, partial, rows, cols, act, s)
-                   : act_grad<DT::BF16, false>(dy, p, u, d0, d1, partial, rows, cols, act, s);
-  if (dtype == HCLRMIX_F16)
-    return aligned ? act_grad<DT::F16, true>(dy, p, u, d0, d1, partial, rows, cols, act, s)
-                   : act_grad<DT::F16, false>(dy, p, u, d0, d1, partial, rows, cols, act, s);
-  return aligned ? act_grad<DT::F32, true>(dy, p, u, d0, d1, partial, rows, cols, act, s)
-                 : act_grad<DT::F32, false>(dy, p, u, d0, d1, partial, rows, cols, act, s);
+  auto run = [&](auto f) { return f(dy, p, u, d0, d1, partial, b0, b1, rows, cols, act, s); };
+  hipError_t e;
+  if (dtype == HCLRMIX_BF16) e = run(aligned ? act_grad<DT::BF16, true> : act_grad<DT::BF16, false>);
+  else if (dtype == HCLRMIX_F16) e = run(aligned ? act_grad<DT::F16, true> : act_grad<DT::F16, false>);
+  else e = run(aligned ? act_grad<DT::F32, true> : act_grad<DT::F32, false>);
+  const int groups = grad_groups(rows);
+  if (e == hipSuccess && partial && groups > 1)
+    e = launch_column_sums(partial, groups, (u ? 2 : 1) * cols, cols, b0, b1, dtype, s);
+  return e;
 }
 
 }  // namespace hc

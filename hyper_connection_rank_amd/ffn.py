@@ -57,6 +57,10 @@ def declare(lib) -> None:
         f.argtypes = sig.get(name, [P, P])
 
 
+_fn = {}   # entry points by name, from the loaded library
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _pkg():
     import hyper_connection_rank_amd as hc
     return hc
@@ -70,25 +74,38 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _entry(name):
+    f = _fn.get(name)
+    if f is None:
+        f = _fn[name] = getattr(_pkg().library(), name)
+    return f
+
+
+def _stream(device):
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _call(name, device, *args):
     """Calls an entry point on the current stream of ``device``, with that device current."""
-    hc = _pkg()
-    f = getattr(hc.library(), name)
+    f = _fn.get(name) or _entry(name)
     if device.type != "cuda":
         _refuse("tensors must be on a GPU", _UNSUPPORTED)
     if device.index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+        status = f(*args, _stream(device))
     else:
         with torch.cuda.device(device):
-            status = f(*args, torch.cuda.current_stream(device).cuda_stream)
+            status = f(*args, _stream(device))
     if status:
-        hc._check(status)
+        _pkg()._check(status)
 
 
 def _size(name, problem) -> int:
-    hc = _pkg()
     n = ctypes.c_size_t()
-    hc._check(getattr(hc.library(), name)(ctypes.byref(problem), ctypes.byref(n)))
+    status = _entry(name)(ctypes.byref(problem), ctypes.byref(n))
+    if status:
+        _pkg()._check(status)
     return n.value
 
 
@@ -162,16 +179,16 @@ def _code(t, name):
 
 
 def _same(t, like, name):
-    if t.dtype != like.dtype or t.device != like.device:
+    if t.dtype is not like.dtype or t.device != like.device:
         _refuse(f"{name} must have the dtype and device of the other tensors")
 
 
 def _matrix(t, like, rows, cols, name) -> int:
     """Checks t's leading dimensions flatten to rows of cols elements; returns the row stride."""
-    _same(t, like, name)
-    n = t.numel()
-    if t.dim() < 1 or t.shape[-1] != cols or n != rows * cols:
-        _refuse(f"{name} must be [..., {cols}] with {rows} rows, got {tuple(t.shape)}")
+    if t is not like:
+        _same(t, like, name)
+        if t.dim() < 1 or t.shape[-1] != cols or t.numel() != rows * cols:
+            _refuse(f"{name} must be [..., {cols}] with {rows} rows, got {tuple(t.shape)}")
     if t.is_contiguous():
         return cols
     if t.stride(-1) != 1 and cols > 1:
@@ -192,6 +209,8 @@ def _dense(t, like, shape, name):
     if t is None:
         return
     _same(t, like, name)
+    if t.shape == shape and t.is_contiguous():
+        return
     n = 1
     for d in shape:
         n *= d
