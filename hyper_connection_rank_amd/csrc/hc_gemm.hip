@@ -57,13 +57,16 @@ struct Gemm {
 __device__ __forceinline__ unsigned* counter_at(unsigned* base, int i) { return base + (i & 31) * 32 + (i >> 5); }
 
 // Chunk permutation of an LDS row: the slot that holds chunk c of row r (and the
-// chunk that slot c holds). Direct tiles (rows of BK): a fragment read takes one
+// chunk that slot c holds). Direct tiles (rows of 128 bytes): a fragment read takes one
 // chunk of 16 consecutive rows, so the low three bits of c change with r.
-// Transposed tiles (rows of R columns): a transposing read takes 32 bytes of rows
-// r .. r+3 and r+8 .. r+11 in one half wave, so whole 32-byte units move with r.
-template <bool TR, int CPR> __device__ __forceinline__ int swz(int r, int c) {
+// Transposed tiles (rows of R columns), 16-bit: a transposing read takes 32 bytes of rows
+// r .. r+3 and r+8 .. r+11 in one half wave, so whole 32-byte units move with r; fp32: a
+// read takes 64 bytes of rows r, r+4, r+8 and r+12, so 64-byte units move with r / 4.
+template <DT D, bool TR, int CPR> __device__ __forceinline__ int swz(int r, int c) {
   if constexpr (!TR) {
     return c ^ (r & 7);
+  } else if constexpr (D == DT::F32) {
+    return c ^ (((r >> 2) & 3) << 2);
   } else if constexpr (CPR >= 16) {
     return c ^ (((r & 3) | ((r >> 1) & 4)) << 1);
   } else {
@@ -71,36 +74,43 @@ template <bool TR, int CPR> __device__ __forceinline__ int swz(int r, int c) {
   }
 }
 
-// One operand's tile: R indices of the output by BK of the contraction.
-template <DT D, bool TR, int R, int BK, int THREADS> struct Tile {
-  static constexpr int CPR = (TR ? R : BK) / 8;  // 16-byte chunks per LDS row
+// One operand's tile: R indices of the output by BK of the contraction (128 bytes).
+template <DT D, bool TR, int R, int THREADS> struct Tile {
+  static constexpr int ES = D == DT::F32 ? 4 : 2, EPC = 16 / ES;  // bytes of an element, elements of a chunk
+  static constexpr int BK = 128 / ES;
+  static constexpr int CPR = (TR ? R : BK) / EPC;  // 16-byte chunks per LDS row
   static constexpr int ROWS = TR ? BK : R;
   static constexpr int NI = ROWS * CPR / THREADS;  // chunks a thread stages
   static constexpr int BYTES = ROWS * CPR * 16;
-  static_assert(ROWS * CPR % THREADS == 0 && CPR >= 8, "tile shape");
+  static constexpr int KSTEP = D == DT::F32 ? 16 : 32;  // contraction indices of one fragment
+  static_assert(ROWS * CPR % THREADS == 0 && CPR >= (D == DT::F32 && TR ? 16 : 8), "tile shape");
+  typedef typename Store<D>::type elem_t;
 
   // Reads this thread's chunks of the tile at output index r0 and contraction
-  // index k0 of an operand with nr output indices and K contraction indices.
-  template <bool ALN>
+  // index k0 of an operand with nr output indices and K contraction indices, at any
+  // element-aligned address.
   static __device__ __forceinline__ void fetch(const void* base, int64_t ld, int64_t r0, int64_t nr, int k0, int K,
                                                int tid, uint4* v) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int c = i * THREADS + tid, row = c / CPR, ch = c % CPR;
-      const int64_t mr = TR ? (int64_t)k0 + row : r0 + row;        // memory row
-      const int64_t mc = TR ? r0 + 8 * ch : (int64_t)k0 + 8 * ch;  // memory column
-      const int64_t left = (TR ? nr : (int64_t)K) - mc;            // columns from here on
+      const int64_t mr = TR ? (int64_t)k0 + row : r0 + row;            // memory row
+      const int64_t mc = TR ? r0 + EPC * ch : (int64_t)k0 + EPC * ch;  // memory column
+      const int64_t left = (TR ? nr : (int64_t)K) - mc;                // columns from here on
       const bool in = mr < (TR ? (int64_t)K : nr) && left > 0;
-      const uint16_t* src = (const uint16_t*)base + mr * ld + mc;
+      const elem_t* src = (const elem_t*)base + mr * ld + mc;
       v[i] = make_uint4(0u, 0u, 0u, 0u);
       if (in) {
-        if (ALN || left >= 8) {
-          v[i] = ld16<D, ALN>(src);
+        if (left >= EPC) {
+          v[i] = ld16<D, false>(src);
         } else {
           uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int e = 0; e < 7; ++e)
-            if (e < left) w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+          for (int e = 0; e < EPC - 1; ++e)
+            if (e < left) {
+              if constexpr (D == DT::F32) w[e] = __float_as_uint(src[e]);
+              else w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
+            }
           v[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
@@ -110,25 +120,38 @@ template <DT D, bool TR, int R, int BK, int THREADS> struct Tile {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int c = i * THREADS + tid, row = c / CPR, ch = c % CPR;
-      *(uint4*)(lds + (row * CPR + swz<TR, CPR>(row, ch)) * 16) = v[i];
+      *(uint4*)(lds + (row * CPR + swz<D, TR, CPR>(row, ch)) * 16) = v[i];
     }
   }
-  // Fragment of output indices r .. r+15 and contraction indices k .. k+31: lane l
-  // holds (r + l % 16, k + 8 (l / 16) + 0..7).
-  static __device__ __forceinline__ s16x8 frag(const unsigned char* lds, int r, int k, int lane) {
+  // Fragment of output indices r .. r+15 and contraction indices k .. k+KSTEP-1. 16-bit: lane l
+  // holds (r + l % 16, k + 8 (l / 16) + 0..7); fp32: (r + l % 16, k + 4 (l / 16) + 0..3), one
+  // value for each of four matrix ops.
+  static __device__ __forceinline__ auto frag(const unsigned char* lds, int r, int k, int lane) {
     const int g = lane >> 4, j = lane & 15;
     if constexpr (!TR) {
       const int row = r + j;
-      return __builtin_bit_cast(s16x8, *(const uint4*)(lds + (row * CPR + swz<TR, CPR>(row, (k >> 3) + g)) * 16));
+      const uint4 v = *(const uint4*)(lds + (row * CPR + swz<D, TR, CPR>(row, k / EPC + g)) * 16);
+      if constexpr (D == DT::F32) return __builtin_bit_cast(f32x4, v);
+      else return __builtin_bit_cast(s16x8, v);
+    } else if constexpr (D == DT::F32) {
+      f32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int kr = k + 4 * g + e;
+        v[e] = *(const float*)(lds + (kr * CPR + swz<D, TR, CPR>(kr, (r >> 2) + (j >> 2))) * 16 + 4 * (j & 3));
+      }
+      return v;
     } else {
       const int kr = k + 8 * g + (j >> 2), cb = j & 3;
-      lds_u8* p = (lds_u8*)(lds + (kr * CPR + swz<TR, CPR>(kr, (r >> 3) + (cb >> 1))) * 16 + 8 * (cb & 1));
+      lds_u8* p = (lds_u8*)(lds + (kr * CPR + swz<D, TR, CPR>(kr, (r >> 3) + (cb >> 1))) * 16 + 8 * (cb & 1));
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * CPR * 16));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   }
 };
+template <DT D> struct Frag { typedef s16x8 type; };
+template <> struct Frag<DT::F32> { typedef f32x4 type; };
 
 // ------------------------------------------------------------------ epilogue
 
@@ -294,82 +317,7 @@ __device__ __forceinline__ Place place(const Gemm& a) {
   return r;
 }
 
-// ------------------------------------------------------------------ 16-bit kernel
-
-// BM x BN tile, WM x WN waves, contraction steps of BK. Dual: the tile's BN
-// columns are BN / 2 of g and the same BN / 2 of u.
-template <DT D, bool PT, bool QT, bool DUAL, int BM, int BN, int BK, int WM, int WN, bool ALN>
-__global__ __launch_bounds__(64 * WM * WN) void k_product(const Gemm a) {
-  constexpr int THREADS = 64 * WM * WN, NQ = DUAL ? 2 : 1;
-  constexpr int FM = BM / WM / 16, FN = BN / WN / 16, FQ = FN / NQ;
-  typedef Tile<D, PT, BM, BK, THREADS> TP;
-  typedef Tile<D, QT, BN / NQ, BK, THREADS> TQ;
-  __shared__ __attribute__((aligned(16))) unsigned char lds[TP::BYTES + NQ * TQ::BYTES];
-  unsigned char* const lq = lds + TP::BYTES;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave / WN, wn = wave % WN;
-  const Place pl = place(a);
-  const int64_t m0 = (int64_t)pl.tm * BM;
-  const int n0 = pl.tn * (BN / NQ);
-
-  f32x4 acc[FM * FN];
-#pragma unroll
-  for (int i = 0; i < FM * FN; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  const int kt = (a.K + BK - 1) / BK, steps = kt * a.segments;
-  const int t0 = (int)((int64_t)steps * pl.split / pl.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / pl.splits);
-  uint4 vp[TP::NI], vq[NQ][TQ::NI];
-  auto fetch = [&](int t) {
-    const int seg = t >= kt, k0 = (t - seg * kt) * BK, b = seg + pl.b;
-    TP::template fetch<ALN>(a.p[b], a.ldp, m0, a.M, k0, a.K, tid, vp);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) TQ::template fetch<ALN>(a.q[b + i], a.ldq, n0, a.N, k0, a.K, tid, vq[i]);
-  };
-  if (t0 < t1) fetch(t0);
-  for (int t = t0; t < t1; ++t) {
-    __syncthreads();
-    TP::put(lds, tid, vp);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) TQ::put(lq + i * TQ::BYTES, tid, vq[i]);
-    __syncthreads();
-    if (t + 1 < t1) fetch(t + 1);
-#pragma unroll
-    for (int k = 0; k < BK; k += 32) {
-      s16x8 fp[FM], fq[FN];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) fp[i] = TP::frag(lds, (wm * FM + i) * 16, k, lane);
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        fq[j] = TQ::frag(lq + (j / FQ) * TQ::BYTES, (wn * FQ + j % FQ) * 16, k, lane);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i * FN + j] = mfma<D>(fq[j], fp[i], acc[i * FN + j]);
-    }
-  }
-
-  if (pl.splits > 1 &&
-      !join_splits<FM * FN, BM, BN>(a, pl.slot, pl.split, m0, acc, tid, [&](int i) { return (wm * FM + i / FN) * 16 + (lane & 15); },
-                                    [&](int i) { return (wn * FN + i % FN) * 4 + (lane >> 4); }))
-    return;
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = m0 + (wm * FM + i) * 16 + (lane & 15);
-#pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      const int n = n0 + (wn * FQ + j) * 16 + 4 * (lane >> 4);
-      float v[4], u[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = acc[i * FN + j][e];
-        if constexpr (DUAL) u[e] = acc[i * FN + FQ + j][e];
-      }
-      finish4<D, DUAL>(a, pl.b, m, n, v, u);
-    }
-  }
-}
-
-// ------------------------------------------------------------------ 16-bit kernel, direct staging
+// ------------------------------------------------------------------ direct staging
 
 // Stages a tile by loads that write LDS themselves: no registers and no LDS
 // write instructions. One instruction per wave fills 1 KB of consecutive LDS,
@@ -396,15 +344,16 @@ template <bool STREAM> __device__ __forceinline__ void lds_load16(u32x4 desc, ui
 
 // Where an operand's next tile starts and how many contraction indices it has from
 // there in its segment; steps go through the first segment, then the second.
-template <bool TR, int BK> struct Cursor {
+template <DT D, bool TR> struct Cursor {
+  static constexpr int ES = D == DT::F32 ? 4 : 2, BK = 128 / ES;
   const char* p;
   const char* p1;  // the second segment's start
   int64_t step;    // bytes from one tile to the next
   int k, k1;
   __device__ __forceinline__ void init(const void* q0, const void* q1, int64_t ld, int64_t r0, int K, int segments, int t,
                                        int steps) {
-    const int64_t first = 2 * (TR ? r0 : r0 * ld);
-    step = 2 * (TR ? BK * ld : (int64_t)BK);
+    const int64_t first = ES * (TR ? r0 : r0 * ld);
+    step = ES * (TR ? BK * ld : (int64_t)BK);
     const int kt = (K + BK - 1) / BK;
     p = (const char*)q0 + first;
     p1 = (const char*)q1 + first;
@@ -433,8 +382,8 @@ template <bool TR, int BK> struct Cursor {
   }
 };
 
-template <bool TR, int R, int BK, int THREADS> struct Direct {
-  typedef Tile<DT::BF16, TR, R, BK, THREADS> T;
+template <DT D, bool TR, int R, int THREADS> struct Direct {
+  typedef Tile<D, TR, R, THREADS> T;
   static constexpr int NI = T::NI;
   static_assert(TR || THREADS / T::CPR % 8 == 0 || NI == 1, "every chunk of a thread has the same place in its row");
   uint32_t off[NI];  // byte offset of this lane's chunks from the tile's first element
@@ -442,11 +391,11 @@ template <bool TR, int R, int BK, int THREADS> struct Direct {
   __device__ __forceinline__ void init(int64_t ld, int64_t r0, int64_t nr, int tid) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int c = i * THREADS + tid, row = c / T::CPR, ch = swz<TR, T::CPR>(row, c % T::CPR);
-      const bool in = TR ? r0 + 8 * ch < nr : r0 + row < nr;
-      off[i] = in ? (uint32_t)(row * (int)ld + 8 * ch) * 2u : OUTSIDE;
+      const int c = i * THREADS + tid, row = c / T::CPR, ch = swz<D, TR, T::CPR>(row, c % T::CPR);
+      const bool in = TR ? r0 + T::EPC * ch < nr : r0 + row < nr;
+      off[i] = in ? (uint32_t)(row * (int)ld + T::EPC * ch) * T::ES : OUTSIDE;
     }
-    kk = TR ? tid / T::CPR : 8 * swz<TR, T::CPR>(tid / T::CPR, tid % T::CPR);
+    kk = TR ? tid / T::CPR : T::EPC * swz<D, TR, T::CPR>(tid / T::CPR, tid % T::CPR);
   }
   // The tile at p, k contraction indices of which exist, into LDS from byte address lds on
   // (this wave's part).
@@ -467,20 +416,30 @@ template <int N> __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
-// BM x BN tile, WM x WN waves, contraction steps of BK staged in a ring of NST buffers: the
+// Workgroup barrier once this wave's LDS operations are done; its global loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// BM x BN tile, WM x WN waves, contraction steps of 128 bytes staged in a ring of NST buffers: the
 // loads of step t + NST - 1 are issued once every wave is done with step t - 1, whose buffer
 // they fill. With many rows two buffers of a 128 x 128 tile (64 KB) leave room for two
 // workgroups per compute unit, whose loads, matrix ops and epilogues overlap. With few rows
 // the product streams its weights: three or more buffers keep about 100 KB of loads in
 // flight per compute unit.
-template <DT D, bool PT, bool QT, bool DUAL, int BM, int BN, int NST, int WM, int WN>
+template <DT D, bool PT, bool QT, bool DUAL, int BM, int BN, int NST, int WM, int WN, bool ALN>
 __global__ __launch_bounds__(64 * WM * WN) void k_product_ring(const Gemm a) {
-  constexpr int THREADS = 64 * WM * WN, NQ = DUAL ? 2 : 1, BK = 64;
+  constexpr int THREADS = 64 * WM * WN, NQ = DUAL ? 2 : 1;
   constexpr int PR = BM < 32 ? 32 : BM;  // staged rows of P: every thread has a chunk; those past M load nothing
   constexpr bool FEW = BM <= 64;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16, FQ = FN / NQ;
-  typedef Tile<D, PT, PR, BK, THREADS> TP;
-  typedef Tile<D, QT, BN / NQ, BK, THREADS> TQ;
+  typedef Tile<D, PT, PR, THREADS> TP;
+  typedef Tile<D, QT, BN / NQ, THREADS> TQ;
+  constexpr int BK = TP::BK, KS = TP::KSTEP;
+  typedef typename Frag<D>::type frag_t;
+  static_assert(ALN || NST == 2, "register staging uses two buffers");
   constexpr int STAGE = TP::BYTES + NQ * TQ::BYTES;
   constexpr int LOADS = TP::NI + NQ * TQ::NI;  // of a wave, per step
   __shared__ __attribute__((aligned(1024))) unsigned char lds[NST * STAGE];
@@ -496,56 +455,115 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product_ring(const Gemm a) {
 
   const int kt = (a.K + BK - 1) / BK, steps = kt * a.segments;
   const int t0 = (int)((int64_t)steps * pl.split / pl.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / pl.splits);
-  Direct<PT, PR, BK, THREADS> dp;
-  Direct<QT, BN / NQ, BK, THREADS> dq;
-  dp.init(a.ldp, m0, BM < PR ? min(a.M, m0 + BM) : a.M, tid);
-  dq.init(a.ldq, n0, a.N, tid);
-  Cursor<PT, BK> cp;
-  Cursor<QT, BK> cq[NQ];
-  cp.init(a.p[pl.b], a.p[1], a.ldp, m0, a.K, a.segments, t0, t1 - t0);
+  // fp32: sums over 512 contraction indices are taken before they are added to the total, so
+  // that the rounding of a long contraction does not grow with its length.
+  constexpr bool BLOCKED = D == DT::F32;
+  f32x4 total[BLOCKED ? FM * FN : 1];
+  if constexpr (BLOCKED) {
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) cq[i].init(a.q[pl.b + i], a.q[1], a.ldq, n0, a.K, a.segments, t0, t1 - t0);
-  const uint32_t l0 = lds_offset(lds);
-  const int w = __builtin_amdgcn_readfirstlane(wave);
-  auto stage = [&](int buf) {
-    const uint32_t to = l0 + buf * STAGE;
-    dp.stage(cp.p, cp.k, to, w);
-    cp.next();
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      if (FEW && a.tiles_m == 1) dq.template stage<true>(cq[i].p, cq[i].k, to + TP::BYTES + i * TQ::BYTES, w);
-      else dq.stage(cq[i].p, cq[i].k, to + TP::BYTES + i * TQ::BYTES, w);
-      cq[i].next();
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < NST - 1; ++i) stage(i);
-  int buf = 0;
-  for (int t = t0; t < t1; ++t) {
-    const unsigned char* cur = lds + buf * STAGE;
+    for (int i = 0; i < FM * FN; ++i) total[i] = acc[i];
+  }
+  auto multiply = [&](const unsigned char* cur, int t) {
     const unsigned char* curq = cur + TP::BYTES;
-    // This wave's loads of step t have arrived and its LDS reads of step t - 1 are done; then
-    // everyone's. Loads past the last step write zeros, so the count in flight is constant.
-    wait_loads<(NST - 2) * LOADS>();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    stage(buf == 0 ? NST - 1 : buf - 1);
-    buf = buf == NST - 1 ? 0 : buf + 1;
 #pragma unroll
-    for (int k = 0; k < BK; k += 32) {
-      s16x8 fp[FM], fq[FN];
+    for (int k = 0; k < BK; k += KS) {
+      frag_t fp[FM], fq[FN];
 #pragma unroll
       for (int j = 0; j < FN; ++j) fq[j] = TQ::frag(curq + (j / FQ) * TQ::BYTES, (wn * FQ + j % FQ) * 16, k, lane);
 #pragma unroll
       for (int i = 0; i < FM; ++i) fp[i] = TP::frag(cur, (wm * FM + i) * 16, k, lane);
+      if constexpr (D == DT::F32) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i * FN + j] = mfma<D>(fq[j], fp[i], acc[i * FN + j]);
+          for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              acc[i * FN + j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fq[j][e], fp[i][e], acc[i * FN + j], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i * FN + j] = mfma<D>(fq[j], fp[i], acc[i * FN + j]);
+      }
+    }
+    if constexpr (BLOCKED) {
+      if (((t - t0) & 15) == 15) {
+#pragma unroll
+        for (int i = 0; i < FM * FN; ++i) {
+          total[i] = total[i] + acc[i];
+          acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+      }
+    }
+  };
+
+  if constexpr (ALN) {
+    Direct<D, PT, PR, THREADS> dp;
+    Direct<D, QT, BN / NQ, THREADS> dq;
+    dp.init(a.ldp, m0, BM < PR ? min(a.M, m0 + BM) : a.M, tid);
+    dq.init(a.ldq, n0, a.N, tid);
+    Cursor<D, PT> cp;
+    Cursor<D, QT> cq[NQ];
+    cp.init(a.p[pl.b], a.p[1], a.ldp, m0, a.K, a.segments, t0, t1 - t0);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) cq[i].init(a.q[pl.b + i], a.q[1], a.ldq, n0, a.K, a.segments, t0, t1 - t0);
+    const uint32_t l0 = lds_offset(lds);
+    const int w = __builtin_amdgcn_readfirstlane(wave);
+    auto stage = [&](int buf) {
+      const uint32_t to = l0 + buf * STAGE;
+      dp.stage(cp.p, cp.k, to, w);
+      cp.next();
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        if (FEW && a.tiles_m == 1) dq.template stage<true>(cq[i].p, cq[i].k, to + TP::BYTES + i * TQ::BYTES, w);
+        else dq.stage(cq[i].p, cq[i].k, to + TP::BYTES + i * TQ::BYTES, w);
+        cq[i].next();
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) stage(i);
+    int buf = 0;
+    for (int t = t0; t < t1; ++t) {
+      // This wave's loads of step t have arrived and its LDS reads of step t - 1 are done; then
+      // everyone's. Loads past the last step write zeros, so the count in flight is constant.
+      wait_loads<(NST - 2) * LOADS>();
+      lds_barrier();
+      stage(buf == 0 ? NST - 1 : buf - 1);
+      multiply(lds + buf * STAGE, t);
+      buf = buf == NST - 1 ? 0 : buf + 1;
+    }
+    wait_loads<0>();  // LDS must not be given up with loads into it in flight
+  } else {
+    // Any element-aligned operand: through registers, the next step's loads issued before
+    // this step's matrix ops and written to the other buffer after them.
+    uint4 vp[TP::NI], vq[NQ][TQ::NI];
+    auto fetch = [&](int t) {
+      const int seg = t >= kt, k0 = (t - seg * kt) * BK, b = seg + pl.b;
+      TP::fetch(a.p[b], a.ldp, m0, BM < PR ? min(a.M, m0 + BM) : a.M, k0, a.K, tid, vp);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) TQ::fetch(a.q[b + i], a.ldq, n0, a.N, k0, a.K, tid, vq[i]);
+    };
+    auto put = [&](int buf) {
+      TP::put(lds + buf * STAGE, tid, vp);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) TQ::put(lds + buf * STAGE + TP::BYTES + i * TQ::BYTES, tid, vq[i]);
+    };
+    fetch(t0);
+    put(0);
+    lds_barrier();
+    for (int t = t0; t < t1; ++t) {
+      const int buf = (t - t0) & 1;
+      if (t + 1 < t1) fetch(t + 1);
+      multiply(lds + buf * STAGE, t);
+      if (t + 1 < t1) put(buf ^ 1);
+      lds_barrier();
     }
   }
-  wait_loads<0>();  // LDS must not be given up with loads into it in flight
+  if constexpr (BLOCKED) {
+#pragma unroll
+    for (int i = 0; i < FM * FN; ++i) acc[i] = total[i] + acc[i];
+  }
 
   if (pl.splits > 1 &&
       !join_splits<FM * FN, BM, BN>(a, pl.slot, pl.split, m0, acc, tid, [&](int i) { return (wm * FM + i / FN) * 16 + (lane & 15); },
@@ -586,8 +604,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product_ring(const Gemm a) {
 template <DT D, bool PT, bool QT, bool DUAL>
 __global__ __launch_bounds__(512) void k_product_wide(const Gemm a) {
   constexpr int THREADS = 512, NQ = DUAL ? 2 : 1, BK = 64, FM = 8, FN = 4, FQ = FN / NQ;
-  typedef Tile<D, PT, 128, BK, THREADS> TP;
-  typedef Tile<D, QT, 256 / NQ, BK, THREADS> TQ;
+  typedef Tile<D, PT, 128, THREADS> TP;
+  typedef Tile<D, QT, 256 / NQ, THREADS> TQ;
   constexpr int QBYTES = NQ * TQ::BYTES, STAGE = QBYTES + 2 * TP::BYTES;
   constexpr int LQ = NQ * TQ::NI, LP = TP::NI;  // loads of a wave for Q, and for half of P
   __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
@@ -603,13 +621,13 @@ __global__ __launch_bounds__(512) void k_product_wide(const Gemm a) {
 
   const int kt = (a.K + BK - 1) / BK, steps = kt * a.segments;
   const int t0 = (int)((int64_t)steps * pl.split / pl.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / pl.splits);
-  Direct<PT, 128, BK, THREADS> dp[2];
-  Direct<QT, 256 / NQ, BK, THREADS> dq;
+  Direct<D, PT, 128, THREADS> dp[2];
+  Direct<D, QT, 256 / NQ, THREADS> dq;
   dp[0].init(a.ldp, m0, a.M, tid);
   dp[1].init(a.ldp, m0 + 128, a.M, tid);
   dq.init(a.ldq, n0, a.N, tid);
-  Cursor<PT, BK> cp[2];
-  Cursor<QT, BK> cq[NQ];
+  Cursor<D, PT> cp[2];
+  Cursor<D, QT> cq[NQ];
 #pragma unroll
   for (int h = 0; h < 2; ++h) cp[h].init(a.p[pl.b], a.p[1], a.ldp, m0 + 128 * h, a.K, a.segments, t0, t1 - t0);
 #pragma unroll
@@ -709,141 +727,6 @@ __global__ __launch_bounds__(512) void k_product_wide(const Gemm a) {
   }
 }
 
-// ------------------------------------------------------------------ fp32 kernel
-
-// The same product in fp32 with 16x16x4 fp32 matrix-core steps. Both operands'
-// tiles sit in LDS as [output index][16 contraction indices], rows 20 floats apart
-// (16 lanes' 16-byte reads then fall on distinct banks); lane l reads contraction
-// indices 4 (l / 16) .. +3 of its row, and step e of four uses the e-th of them.
-// Sums over 512 contraction indices are taken before they are added to the total,
-// so that a long contraction's rounding grows with its square root at a slower rate.
-template <bool TR, int R, int THREADS> struct Tile32 {
-  static constexpr int LD = 20;
-  static constexpr int BK = 16;
-  static constexpr int CHUNKS = R * BK / 4;  // four floats each
-  static constexpr int NI = (CHUNKS + THREADS - 1) / THREADS;
-
-  static __device__ __forceinline__ void fetch(const void* base, int64_t ld, int64_t r0, int64_t nr, int k0, int K,
-                                               bool aln, int tid, f32x4* v) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int c = i * THREADS + tid;
-      const int row = TR ? c / (R / 4) : c / 4, ch = TR ? c % (R / 4) : c % 4;
-      const int64_t mr = TR ? (int64_t)k0 + row : r0 + row;
-      const int64_t mc = TR ? r0 + 4 * ch : (int64_t)k0 + 4 * ch;
-      const int64_t left = (TR ? nr : (int64_t)K) - mc;
-      const float* src = (const float*)base + mr * ld + mc;
-      v[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (c < CHUNKS && mr < (TR ? (int64_t)K : nr) && left > 0) {
-        if (aln) {
-          v[i] = *(const f32x4*)src;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < left) v[i][e] = src[e];
-        }
-      }
-    }
-  }
-  static __device__ __forceinline__ void put(float* lds, int tid, const f32x4* v) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int c = i * THREADS + tid;
-      if (c < CHUNKS) {
-        if constexpr (!TR) {
-          *(f32x4*)(lds + (c / 4) * LD + 4 * (c % 4)) = v[i];
-        } else {
-          const int k = c / (R / 4), r = 4 * (c % (R / 4));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) lds[(r + e) * LD + k] = v[i][e];
-        }
-      }
-    }
-  }
-  static __device__ __forceinline__ f32x4 frag(const float* lds, int r, int lane) {
-    return *(const f32x4*)(lds + (r + (lane & 15)) * LD + 4 * (lane >> 4));
-  }
-};
-
-template <bool PT, bool QT, bool DUAL, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void k_product32(const Gemm a, const bool aln) {
-  constexpr int THREADS = 64 * WM * WN, NQ = DUAL ? 2 : 1, BK = 16;
-  constexpr int FM = BM / WM / 16, FN = BN / WN / 16, FQ = FN / NQ, NA = FM * FN;
-  typedef Tile32<PT, BM, THREADS> TP;
-  typedef Tile32<QT, BN / NQ, THREADS> TQ;
-  __shared__ __attribute__((aligned(16))) float lds[(BM + BN) * TP::LD];
-  float* const lq = lds + BM * TP::LD;
-  constexpr int LQ = (BN / NQ) * TP::LD;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave / WN, wn = wave % WN;
-  const Place pl = place(a);
-  const int64_t m0 = (int64_t)pl.tm * BM;
-  const int n0 = pl.tn * (BN / NQ);
-
-  f32x4 acc[NA], tot[NA];
-#pragma unroll
-  for (int i = 0; i < NA; ++i) acc[i] = tot[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int kt = (a.K + BK - 1) / BK, steps = kt * a.segments;
-  const int t0 = (int)((int64_t)steps * pl.split / pl.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / pl.splits);
-  f32x4 vp[TP::NI], vq[NQ][TQ::NI];
-  auto fetch = [&](int t) {
-    const int seg = t >= kt, k0 = (t - seg * kt) * BK, b = seg + pl.b;
-    TP::fetch(a.p[b], a.ldp, m0, a.M, k0, a.K, aln, tid, vp);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) TQ::fetch(a.q[b + i], a.ldq, n0, a.N, k0, a.K, aln, tid, vq[i]);
-  };
-  if (t0 < t1) fetch(t0);
-  for (int t = t0; t < t1; ++t) {
-    __syncthreads();
-    TP::put(lds, tid, vp);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) TQ::put(lq + i * LQ, tid, vq[i]);
-    __syncthreads();
-    if (t + 1 < t1) fetch(t + 1);
-    f32x4 fp[FM], fq[FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) fp[i] = TP::frag(lds, (wm * FM + i) * 16, lane);
-#pragma unroll
-    for (int j = 0; j < FN; ++j) fq[j] = TQ::frag(lq + (j / FQ) * LQ, (wn * FQ + j % FQ) * 16, lane);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i * FN + j] = __builtin_amdgcn_mfma_f32_16x16x4f32(fq[j][e], fp[i][e], acc[i * FN + j], 0, 0, 0);
-    if (((t - t0) & 31) == 31) {
-#pragma unroll
-      for (int i = 0; i < NA; ++i) {
-        tot[i] = tot[i] + acc[i];
-        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NA; ++i) acc[i] = tot[i] + acc[i];
-
-  if (pl.splits > 1 &&
-      !join_splits<NA, BM, BN>(a, pl.slot, pl.split, m0, acc, tid, [&](int i) { return (wm * FM + i / FN) * 16 + (lane & 15); },
-                                    [&](int i) { return (wn * FN + i % FN) * 4 + (lane >> 4); }))
-    return;
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = m0 + (wm * FM + i) * 16 + (lane & 15);
-#pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      const int n = n0 + (wn * FQ + j) * 16 + 4 * (lane >> 4);
-      float v[4], u[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = acc[i * FN + j][e];
-        if constexpr (DUAL) u[e] = acc[i * FN + FQ + j][e];
-      }
-      finish4<DT::F32, DUAL>(a, pl.b, m, n, v, u);
-    }
-  }
-}
-
 // ------------------------------------------------------------------ schedule
 
 constexpr int CUS = 256;
@@ -869,11 +752,11 @@ struct Plan {
 // A shape's tiles run in rounds of `slots` workgroups. Full rounds take their tiles whole; the
 // tiles left over (all of them, where there are fewer than slots) are split along the
 // contraction where that ends sooner: parts run shorter, but they are written and read again,
-// and the last one to arrive reads them all. The shapes' times were fitted to 3,600 measured
-// combinations of shape, split and product (1 to 8192 rows; five weights from 1024 x 1024 to
-// 10240 x 2560; all three operand layouts): the model is within 12 % of one standard deviation
-// of the measured times, and the plan it picks within 3 % of the best one measured on average
-// (30 % at worst).
+// and the last one to arrive reads them all. The shapes' times were fitted to 8,500 measured
+// combinations of shape, split and product (1 to 8192 rows; ten weights from 2000 x 160 to
+// 10240 x 2560; all three operand layouts, aligned and not, bf16 and fp32): the model's error
+// has a standard deviation of about 12 %, and the plans it picks took 3 % more time on average
+// than the best ones measured (56 % at worst).
 static Plan shape_plan(const Shape& sh, int64_t M, int64_t N, int64_t K, bool dual, int segments, int batch) {
   Plan p{};
   p.shape = &sh;
@@ -916,14 +799,22 @@ constexpr Shape F64W{64, 256, 64, 256, 0.722, 0.735, 5.175, 0.544, 6.2};
 constexpr Shape F16{16, 64, 64, 768, 0.862, 0.175, 5.099, 0.083, 7.3};
 constexpr Shape F16D{16, 128, 64, 512, 1.310, 0.709, 1.857, 0.423, 3.1};
 constexpr Shape F16W{16, 256, 64, 256, 0.737, 0.626, 4.047, 0.419, 2.4};
-// Register-staged kernels, for operands that are not 16-byte aligned.
-constexpr Shape U128{128, 128, 64, 512, 2.0, 1.0, 4.0, 0.6, 6.0};
-constexpr Shape U16{16, 64, 128, 768, 2.0, 1.0, 3.0, 0.1, 6.0};
-constexpr Shape U16D{16, 128, 128, 768, 4.0, 1.0, 3.0, 0.1, 6.0};
-// fp32.
-constexpr Shape S128{128, 128, 16, 512, 3.0, 1.0, 4.0, 0.6, 6.0};
-constexpr Shape S16{16, 64, 16, 768, 0.2, 0.2, 3.0, 0.1, 6.0};
-constexpr Shape S16D{16, 128, 16, 768, 0.4, 0.2, 3.0, 0.1, 6.0};
+// Operands that are not 16-byte aligned, fp32, and both.
+constexpr Shape U128{128, 128, 64, 512, 1.682, 1.934, 4.764, 0.518, 5.0};
+constexpr Shape U64{64, 64, 64, 1024, 1.908, 0.857, 4.768, 0.302, 6.7};
+constexpr Shape U64D{64, 128, 64, 768, 2.191, 1.832, 2.396, 0.705, 6.7};
+constexpr Shape U16{16, 64, 64, 1024, 1.829, 0.744, 4.963, 0.118, 4.2};
+constexpr Shape U16D{16, 128, 64, 768, 2.700, 1.436, 2.938, 0.241, 20.0};
+constexpr Shape S128{128, 128, 32, 512, 4.129, 2.306, 5.816, 0.491, 6.3};
+constexpr Shape S64{64, 64, 32, 768, 1.859, 0.818, 4.282, 0.352, 9.4};
+constexpr Shape S64D{64, 128, 32, 512, 2.369, 1.428, 4.227, 0.696, 10.4};
+constexpr Shape S16{16, 64, 32, 768, 0.968, 0.378, 6.002, 0.093, 20.0};
+constexpr Shape S16D{16, 128, 32, 512, 1.163, 0.053, 5.300, 0.182, 20.0};
+constexpr Shape V128{128, 128, 32, 256, 3.058, 3.541, 3.581, 0.499, 4.5};
+constexpr Shape V64{64, 64, 32, 1024, 3.223, 1.271, 4.156, 0.336, 6.6};
+constexpr Shape V64D{64, 128, 32, 512, 3.248, 2.506, 1.765, 0.751, 7.9};
+constexpr Shape V16{16, 64, 32, 1024, 2.101, 0.910, 4.773, 0.109, 20.0};
+constexpr Shape V16D{16, 128, 32, 768, 2.923, 1.608, 3.016, 0.208, 20.0};
 
 static Plan make_plan(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch,
                       bool aln) {
@@ -932,21 +823,19 @@ static Plan make_plan(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, 
     const Plan p = shape_plan(s, M, N, K, dual, segments, batch);
     if (!best.shape || p.us < best.us) best = p;
   };
-  const bool few = M <= 16 && !p_trans;
-  if (dtype == HCLRMIX_F32) {
-    consider(few ? (dual ? S16D : S16) : S128);
-  } else if (!aln) {
-    consider(few ? (dual ? U16D : U16) : U128);
+  const bool f32 = dtype == HCLRMIX_F32, few = M <= 16 && !p_trans;
+  if (f32 || !aln) {
+    consider(!f32 ? U128 : aln ? S128 : V128);
+    consider(!f32 ? (dual ? U64D : U64) : aln ? (dual ? S64D : S64) : (dual ? V64D : V64));
+    if (few) consider(!f32 ? (dual ? U16D : U16) : aln ? (dual ? S16D : S16) : (dual ? V16D : V16));
   } else {
     consider(MID);
     consider(WIDE);
-    if (!p_trans) {
-      consider(dual ? F64D : F64);
-      consider(F64W);
-      if (M <= 16) {
-        consider(dual ? F16D : F16);
-        consider(F16W);
-      }
+    consider(dual ? F64D : F64);
+    if (!p_trans) consider(F64W);
+    if (few) {
+      consider(dual ? F16D : F16);
+      consider(F16W);
     }
   }
   return best;
@@ -962,36 +851,34 @@ size_t product_scratch(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans,
   return most;
 }
 
+// k_product_ring for one tile shape.
+template <DT D, bool PT, bool QT, bool DUAL, int BM, int BN, int NST, int WM, int WN, bool ALN>
+static hipError_t ring(const Gemm& g, unsigned n, hipStream_t s) {
+  return launch(nullptr, k_product_ring<D, PT, QT, DUAL, BM, BN, NST, WM, WN, ALN>, dim3(n), dim3(64 * WM * WN), 0, s, g);
+}
+
 template <DT D, bool PT, bool QT, bool DUAL>
-static hipError_t go16(const Gemm& g, const Shape& sh, bool aln, unsigned n, hipStream_t s) {
-  const dim3 grid(n), wg(256);
+static hipError_t go(const Gemm& g, const Shape& sh, bool aln, unsigned n, hipStream_t s) {
+  constexpr int BN = DUAL ? 128 : 64;
   if constexpr (!PT) {
-    constexpr int BN = DUAL ? 128 : 64;
-    if (!aln && sh.bm == 16) return launch(nullptr, k_product<D, PT, QT, DUAL, 16, BN, 128, 1, 4, false>, grid, wg, 0, s, g);
-    if (sh.bm == 16 && sh.bn == 256) return launch(nullptr, k_product_ring<D, PT, QT, DUAL, 16, 256, 3, 1, 4>, grid, wg, 0, s, g);
-    if (sh.bm == 16) return launch(nullptr, k_product_ring<D, PT, QT, DUAL, 16, BN, DUAL ? 3 : 4, 1, 4>, grid, wg, 0, s, g);
-    if (sh.bm == 64 && sh.bn == 256) return launch(nullptr, k_product_ring<D, PT, QT, DUAL, 64, 256, 3, 1, 4>, grid, wg, 0, s, g);
-    if (sh.bm == 64) return launch(nullptr, k_product_ring<D, PT, QT, DUAL, 64, BN, 3, 2, 2>, grid, wg, 0, s, g);
+    if (sh.bm == 16 && !aln) return ring<D, PT, QT, DUAL, 16, BN, 2, 1, 4, false>(g, n, s);
+    if constexpr (D != DT::F32) {
+      if (sh.bm == 16 && sh.bn == 256) return ring<D, PT, QT, DUAL, 16, 256, 3, 1, 4, true>(g, n, s);
+      if (sh.bm == 64 && sh.bn == 256) return ring<D, PT, QT, DUAL, 64, 256, 3, 1, 4, true>(g, n, s);
+    }
+    if (sh.bm == 16) return ring<D, PT, QT, DUAL, 16, BN, DUAL ? 3 : 4, 1, 4, true>(g, n, s);
   }
-  if (sh.bm == 256) return launch(nullptr, k_product_wide<D, PT, QT, DUAL>, grid, dim3(512), 0, s, g);
-  return aln ? launch(nullptr, k_product_ring<D, PT, QT, DUAL, 128, 128, 2, 2, 2>, grid, wg, 0, s, g)
-             : launch(nullptr, k_product<D, PT, QT, DUAL, 128, 128, 64, 2, 2, false>, grid, wg, 0, s, g);
+  if (sh.bm == 64) return aln ? ring<D, PT, QT, DUAL, 64, BN, 3, 2, 2, true>(g, n, s) : ring<D, PT, QT, DUAL, 64, BN, 2, 2, 2, false>(g, n, s);
+  if constexpr (D != DT::F32) {
+    if (sh.bm == 256) return launch(nullptr, k_product_wide<D, PT, QT, DUAL>, dim3(n), dim3(512), 0, s, g);
+  }
+  return aln ? ring<D, PT, QT, DUAL, 128, 128, 2, 2, 2, true>(g, n, s) : ring<D, PT, QT, DUAL, 128, 128, 2, 2, 2, false>(g, n, s);
 }
 
-template <bool PT, bool QT, bool DUAL>
-static hipError_t go32(const Gemm& g, const Shape& sh, bool aln, unsigned n, hipStream_t s) {
-  const dim3 grid(n), wg(256);
-  if constexpr (!PT) {
-    if (sh.bm == 16) return launch(nullptr, k_product32<PT, QT, DUAL, 16, DUAL ? 128 : 64, 1, 4>, grid, wg, 0, s, g, aln);
-  }
-  return launch(nullptr, k_product32<PT, QT, DUAL, 128, 128, 2, 2>, grid, wg, 0, s, g, aln);
-}
-
-template <bool PT, bool QT, bool DUAL>
-static hipError_t go(const Gemm& g, const Shape& p, int dtype, bool aln, unsigned grid, hipStream_t s) {
-  if (dtype == HCLRMIX_F32) return go32<PT, QT, DUAL>(g, p, aln, grid, s);
-  return dtype == HCLRMIX_BF16 ? go16<DT::BF16, PT, QT, DUAL>(g, p, aln, grid, s)
-                               : go16<DT::F16, PT, QT, DUAL>(g, p, aln, grid, s);
+template <DT D> static hipError_t go_layout(const Product& p, const Gemm& g, const Shape& sh, bool aln, unsigned n, hipStream_t s) {
+  if (p.dual) return go<D, false, true, true>(g, sh, aln, n, s);
+  if (p.p_trans) return go<D, true, true, false>(g, sh, aln, n, s);
+  return p.q_trans ? go<D, false, true, false>(g, sh, aln, n, s) : go<D, false, false, false>(g, sh, aln, n, s);
 }
 
 hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* counters, hipStream_t s) {
@@ -1033,9 +920,9 @@ hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* 
   const int64_t grid = pl.whole + pl.rest * pl.splits;
   if (grid > 0x3FFFFF) return hipErrorInvalidValue;
   const unsigned n = (unsigned)grid;
-  if (p.dual) return go<false, true, true>(g, *pl.shape, dtype, aln, n, s);
-  if (p.p_trans) return go<true, true, false>(g, *pl.shape, dtype, aln, n, s);
-  return p.q_trans ? go<false, true, false>(g, *pl.shape, dtype, aln, n, s) : go<false, false, false>(g, *pl.shape, dtype, aln, n, s);
+  if (dtype == HCLRMIX_F32) return go_layout<DT::F32>(p, g, *pl.shape, aln, n, s);
+  return dtype == HCLRMIX_BF16 ? go_layout<DT::BF16>(p, g, *pl.shape, aln, n, s)
+                               : go_layout<DT::F16>(p, g, *pl.shape, aln, n, s);
 }
 
 // ------------------------------------------------------------------ activation gradients
