@@ -927,12 +927,10 @@ hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* 
 
 // ------------------------------------------------------------------ activation gradients
 
-constexpr int GRAD_ROWS = 64;  // rows per group, at least
-
-int grad_groups(int64_t rows) {
-  const int64_t g = (rows + GRAD_ROWS - 1) / GRAD_ROWS;
-  return (int)(g < 64 ? g : 64);
-}
+// One group up to 64 rows (its sums are the result, without a second launch), then one for
+// every 16 rows up to 128 groups, so that few columns still fill the chip (2011 x 4096: 18.9 us
+// with 32 groups).
+int grad_groups(int64_t rows) { return rows <= 64 ? 1 : (int)std::min<int64_t>((rows + 15) / 16, 128); }
 
 // A thread takes eight columns of its group's rows (a contiguous range),
 // ascending, and holds their column sums. With one group the sums are the
