@@ -13,8 +13,8 @@
 // transposed operand's fragments come from the transposing LDS read.
 //
 // The matrix op is given Q's fragment as its first operand, so a lane's result
-// holds four consecutive columns n of one row m: bias, residual and the stores of
-// the epilogue are then one 8-byte access per four elements.
+// holds four consecutive columns n of one row m: one 16-byte access per vector
+// where sums go to LDS or scratch.
 //
 // Few tiles: the contraction is split over workgroups. Each writes its fp32 tile
 // to scratch with agent-coherent stores and counts itself in; the last one adds
@@ -48,7 +48,7 @@ struct Gemm {
   int tiles_m, tiles_n;
   int whole;        // tiles taken by one workgroup each (the first ones); the rest are split
   int splits;       // parts of a split tile
-  int vec4;         // four consecutive columns of every [M, N] tensor and bias are 4-element aligned
+  int vec8;         // N is a multiple of 8 and every [M, N] tensor and bias 16-byte aligned
   float* partial;   // [split tile][split][BM * BN] fp32
   unsigned* counters;
 };
@@ -155,72 +155,74 @@ template <> struct Frag<DT::F32> { typedef f32x4 type; };
 
 // ------------------------------------------------------------------ epilogue
 
-// Four consecutive elements of a row, n of them valid.
-template <DT D> __device__ __forceinline__ void ld4(const void* base, int64_t i, int n, bool vec, float* x) {
-  if (vec && n >= 4) {
-    if constexpr (D == DT::F32) {
-      const f32x4 v = *(const f32x4*)((const float*)base + i);
+// The tile's fp32 sums go through LDS once more, so that every global access of the epilogue is
+// eight consecutive elements of a row and neighbouring lanes follow each other: whole cache
+// lines. (Stores straight from the matrix-core layout, four elements of 16 rows per
+// instruction, write 32 bytes of a line at a time.)
+
+// Eight columns n .. n+7 of row m: v (and u of a dual product) hold the fp32 sums.
+template <DT D, bool DUAL, bool ALN>
+__device__ __forceinline__ void finish8(const Gemm& a, int b, int64_t m, int n, float* v, float* u) {
+  const int left = a.N - n;
+  const int64_t i = m * a.N + n;
+  float t[8];
+  if (a.bias[0]) {
+    load8<D, ALN>(a.bias[0], n, left, t);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = v[e];
-    } else {
-      unpack4<D>(*(const u32x2*)((const uint16_t*)base + i), x);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = e < n ? ld<D>(base, i + e) : 0.0f;
+    for (int e = 0; e < 8; ++e) v[e] = v[e] + t[e];
   }
-}
-template <DT D> __device__ __forceinline__ void st4(void* base, int64_t i, int n, bool vec, const float* x) {
-  if (vec && n >= 4) {
-    if constexpr (D == DT::F32) *(f32x4*)((float*)base + i) = f32x4{x[0], x[1], x[2], x[3]};
-    else *(u32x2*)((uint16_t*)base + i) = u32x2{pack2<D>(x[0], x[1]), pack2<D>(x[2], x[3])};
-  } else {
+  if constexpr (DUAL) {
+    if (a.bias[1]) {
+      load8<D, ALN>(a.bias[1], n, left, t);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) st<D>(base, i + e, x[e]);
+      for (int e = 0; e < 8; ++e) u[e] = u[e] + t[e];
+    }
+    if (a.save[0]) {
+      store8<D, ALN>(a.save[0], i, left, v);
+      store8<D, ALN>(a.save[1], i, left, u);
+    }
+    act_n<D, 8>(a.act, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * u[e];
+    store8<D, ALN>(a.out[0], i, left, v);
+  } else {
+    if (a.save[0]) store8<D, ALN>(a.save[0], i, left, v);
+    act_n<D, 8>(a.act, v);
+    if (a.residual) {
+      load8<D, ALN>(a.residual, m * a.ldr + n, left, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] + t[e];
+    }
+    store8<D, ALN>(a.out[b], i, left, v);
   }
 }
 
-// Columns n .. n+3 of row m: v (and u of a dual product) hold the fp32 sums.
-template <DT D, bool DUAL>
-__device__ __forceinline__ void finish4(const Gemm& a, int b, int64_t m, int n, float* v, float* u) {
-  const int left = a.N - n;
-  if (m >= a.M || left <= 0) return;
-  const int64_t i = m * a.N + n;
-  float t[4];
-  if constexpr (DUAL) {
-    if (a.bias[0]) {
-      ld4<D>(a.bias[0], n, left, a.vec4, t);
+// Place of column quad c (four floats) of row r in the LDS image of [rows][BN] sums: the quads
+// of 16 consecutive rows, which one write instruction covers, fall on distinct banks.
+template <int BN> __device__ __forceinline__ int sum_at(int r, int c) { return r * BN + 4 * (c ^ (r & 15)); }
+
+// Rows m0 .. m0+ROWS-1, columns from n0 on, from their LDS image (after a barrier).
+template <DT D, bool DUAL, int ROWS, int BN, int THREADS>
+__device__ __forceinline__ void finish_rows(const Gemm& a, int b, const float* sums, int64_t m0, int n0, int tid) {
+  constexpr int COLS = DUAL ? BN / 2 : BN, CH = COLS / 8;  // chunks of eight output columns per row
+  const int rows = (int)min((int64_t)ROWS, a.M - m0);
+  for (int i = tid; i < rows * CH; i += THREADS) {
+    const int r = i / CH, c = i - r * CH, n = n0 + 8 * c;
+    if (n >= a.N) continue;
+    float v[8], u[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = v[e] + t[e];
-    }
-    if (a.bias[1]) {
-      ld4<D>(a.bias[1], n, left, a.vec4, t);
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 x = *(const f32x4*)(sums + sum_at<BN>(r, 2 * c + h));
+      f32x4 y = x;
+      if constexpr (DUAL) y = *(const f32x4*)(sums + sum_at<BN>(r, COLS / 4 + 2 * c + h));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = u[e] + t[e];
+      for (int e = 0; e < 4; ++e) {
+        v[4 * h + e] = x[e];
+        u[4 * h + e] = y[e];
+      }
     }
-    if (a.save[0]) {
-      st4<D>(a.save[0], i, left, a.vec4, v);
-      st4<D>(a.save[1], i, left, a.vec4, u);
-    }
-    act_n<D, 4>(a.act, v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = v[e] * u[e];
-    st4<D>(a.out[0], i, left, a.vec4, v);
-  } else {
-    if (a.bias[0]) {
-      ld4<D>(a.bias[0], n, left, a.vec4, t);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = v[e] + t[e];
-    }
-    if (a.save[0]) st4<D>(a.save[0], i, left, a.vec4, v);
-    act_n<D, 4>(a.act, v);
-    if (a.residual) {
-      ld4<D>(a.residual, m * a.ldr + n, left, a.vec4, t);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = v[e] + t[e];
-    }
-    st4<D>(a.out[b], i, left, a.vec4, v);
+    if (a.vec8) finish8<D, DUAL, true>(a, b, m0 + r, n, v, u);
+    else finish8<D, DUAL, false>(a, b, m0 + r, n, v, u);
   }
 }
 
@@ -565,25 +567,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product_ring(const Gemm a) {
     for (int i = 0; i < FM * FN; ++i) acc[i] = total[i] + acc[i];
   }
 
+  // Column quad of vector i in the tile: the columns of Q0, then those of Q1.
+  auto quad = [&](int i) {
+    const int j = i % FN;
+    return ((j / FQ) * (BN / NQ) + (wn * FQ + j % FQ) * 16) / 4 + (lane >> 4);
+  };
   if (pl.splits > 1 &&
       !join_splits<FM * FN, BM, BN>(a, pl.slot, pl.split, m0, acc, tid, [&](int i) { return (wm * FM + i / FN) * 16 + (lane & 15); },
-                                    [&](int i) { return (wn * FN + i % FN) * 4 + (lane >> 4); }))
+                                    quad))
     return;
+  static_assert(BM * BN * 4 <= NST * STAGE, "the sums fit the staging buffers");
+  float* const sums = (float*)lds;
+  lds_barrier();
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = m0 + (wm * FM + i) * 16 + (lane & 15);
-#pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      const int n = n0 + (wn * FQ + j) * 16 + 4 * (lane >> 4);
-      float v[4], u[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = acc[i * FN + j][e];
-        if constexpr (DUAL) u[e] = acc[i * FN + FQ + j][e];
-      }
-      finish4<D, DUAL>(a, pl.b, m, n, v, u);
-    }
-  }
+  for (int i = 0; i < FM * FN; ++i)
+    *(f32x4*)(sums + sum_at<BN>((wm * FM + i / FN) * 16 + (lane & 15), quad(i))) = acc[i];
+  lds_barrier();
+  finish_rows<D, DUAL, BM, BN, THREADS>(a, pl.b, sums, m0, n0, tid);
 }
 
 // 256 x 256 tile, contraction steps of 64, eight waves, for products with many tiles. Wave
@@ -706,24 +706,24 @@ __global__ __launch_bounds__(512) void k_product_wide(const Gemm a) {
   }
   wait_loads<0>();  // LDS must not be given up with loads into it in flight
 
+  // Column quad of vector i in the tile: the columns of Q0, then those of Q1.
+  auto quad = [&](int i) {
+    const int j = i % FN;
+    return ((j / FQ) * (256 / NQ) + (wn * FQ + j % FQ) * 16) / 4 + (lane >> 4);
+  };
   if (pl.splits > 1 &&
       !join_splits<FM * FN, 256, 256>(a, pl.slot, pl.split, m0, acc, tid, [&](int i) { return (i / FN / 4) * 128 + (wm * 4 + i / FN % 4) * 16 + (lane & 15); },
-                                    [&](int i) { return (wn * FN + i % FN) * 4 + (lane >> 4); }))
+                                    quad))
     return;
+  float* const sums = (float*)lds;  // 128 rows at a time
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = m0 + (i / 4) * 128 + (wm * 4 + i % 4) * 16 + (lane & 15);
+  for (int half = 0; half < 2; ++half) {
+    lds_barrier();
 #pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      const int n = n0 + (wn * FQ + j) * 16 + 4 * (lane >> 4);
-      float v[4], u[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = acc[i * FN + j][e];
-        if constexpr (DUAL) u[e] = acc[i * FN + FQ + j][e];
-      }
-      finish4<D, DUAL>(a, pl.b, m, n, v, u);
-    }
+    for (int i = 0; i < FM * FN / 2; ++i)
+      *(f32x4*)(sums + sum_at<256>((wm * 4 + i / FN) * 16 + (lane & 15), quad(i))) = acc[half * FM * FN / 2 + i];
+    lds_barrier();
+    finish_rows<D, DUAL, 128, 256, THREADS>(a, pl.b, sums, m0 + 128 * half, n0, tid);
   }
 }
 
@@ -888,7 +888,7 @@ hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* 
   // 16-byte accesses: rows start on them and their ends do too.
   bool aln = p.ldp % a16 == 0 && p.ldq % a16 == 0 && (p.p_trans ? p.M : (int64_t)p.K) % (int64_t)a16 == 0 &&
              (p.q_trans ? p.N : p.K) % (int64_t)a16 == 0;
-  bool v4 = p.N % 4 == 0 && (!p.residual || p.ldr % 4 == 0);
+  bool v8 = p.N % 8 == 0 && (!p.residual || p.ldr % (int64_t)a16 == 0);
   auto on = [](const void* q, uintptr_t to) { return ((uintptr_t)q & (to - 1)) == 0; };
   for (int i = 0; i < 2; ++i) {
     g.p[i] = p.p[i];
@@ -897,9 +897,9 @@ hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* 
     g.out[i] = p.out[i];
     g.save[i] = p.save[i];
     aln = aln && on(p.p[i], 16) && on(p.q[i], 16);
-    v4 = v4 && on(p.bias[i], 4 * es) && on(p.out[i], 4 * es) && on(p.save[i], 4 * es);
+    v8 = v8 && on(p.bias[i], 16) && on(p.out[i], 16) && on(p.save[i], 16);
   }
-  v4 = v4 && on(p.residual, 4 * es);
+  v8 = v8 && on(p.residual, 16);
   const Plan pl = make_plan(dtype, p.M, p.N, p.K, p.p_trans, p.dual, p.segments, p.batch, aln);
   g.ldp = p.ldp;
   g.ldq = p.ldq;
@@ -914,7 +914,7 @@ hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* 
   g.tiles_n = pl.tiles_n;
   g.whole = (int)pl.whole;
   g.splits = pl.splits;
-  g.vec4 = v4;
+  g.vec8 = v8;
   g.partial = (float*)scratch;
   g.counters = counters;
   const int64_t grid = pl.whole + pl.rest * pl.splits;
