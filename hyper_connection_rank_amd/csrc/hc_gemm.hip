@@ -165,17 +165,22 @@ template <DT D, bool DUAL, bool ALN>
 __device__ __forceinline__ void finish8(const Gemm& a, int b, int64_t m, int n, float* v, float* u) {
   const int left = a.N - n;
   const int64_t i = m * a.N + n;
-  float t[8];
+  // Every load first: one memory latency for all.
+  float t[8], w[8];
+  if (a.bias[0]) load8<D, ALN>(a.bias[0], n, left, t);
+  if constexpr (DUAL) {
+    if (a.bias[1]) load8<D, ALN>(a.bias[1], n, left, w);
+  } else {
+    if (a.residual) load8<D, ALN>(a.residual, m * a.ldr + n, left, w);
+  }
   if (a.bias[0]) {
-    load8<D, ALN>(a.bias[0], n, left, t);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = v[e] + t[e];
   }
   if constexpr (DUAL) {
     if (a.bias[1]) {
-      load8<D, ALN>(a.bias[1], n, left, t);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = u[e] + t[e];
+      for (int e = 0; e < 8; ++e) u[e] = u[e] + w[e];
     }
     if (a.save[0]) {
       store8<D, ALN>(a.save[0], i, left, v);
@@ -189,9 +194,8 @@ __device__ __forceinline__ void finish8(const Gemm& a, int b, int64_t m, int n, 
     if (a.save[0]) store8<D, ALN>(a.save[0], i, left, v);
     act_n<D, 8>(a.act, v);
     if (a.residual) {
-      load8<D, ALN>(a.residual, m * a.ldr + n, left, t);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] + t[e];
+      for (int e = 0; e < 8; ++e) v[e] = v[e] + w[e];
     }
     store8<D, ALN>(a.out[b], i, left, v);
   }
@@ -796,7 +800,7 @@ constexpr Shape MID{128, 128, 64, 512, 1.211, 0.787, 4.645, 0.607, 6.5};
 constexpr Shape F64{64, 64, 64, 768, 0.826, 0.347, 3.790, 0.422, 13.1};
 constexpr Shape F64D{64, 128, 64, 512, 1.164, 0.694, 1.541, 0.918, 9.6};
 constexpr Shape F64W{64, 256, 64, 256, 0.722, 0.735, 5.175, 0.544, 6.2};
-constexpr Shape F16{16, 64, 64, 768, 0.862, 0.175, 5.099, 0.083, 7.3};
+constexpr Shape F16{16, 64, 64, 768, 0.862, 0.400, 5.099, 0.083, 7.3};
 constexpr Shape F16D{16, 128, 64, 512, 1.310, 0.709, 1.857, 0.423, 3.1};
 constexpr Shape F16W{16, 256, 64, 256, 0.737, 0.626, 4.047, 0.419, 2.4};
 // Operands that are not 16-byte aligned, fp32, and both.
