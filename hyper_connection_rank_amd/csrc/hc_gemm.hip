@@ -336,11 +336,18 @@ __device__ __forceinline__ u32x4 raw_desc(const void* base) {
                (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)), 0x7FFFFFF0u, 0x00020000u};
 }
 __device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(const lds_u8*)p; }
-// Lane l: 16 bytes from offset off of the descriptor to LDS byte dst + 16 l (dst the
-// same in every lane). Written out because the compiler, which cannot tell the stage
+// Lane l: W bytes (16 or 4) from offset off of the descriptor to LDS byte dst + W l (dst
+// the same in every lane). Written out because the compiler, which cannot tell the stage
 // being filled from the one being read, would wait for the load before every LDS read.
-template <bool STREAM> __device__ __forceinline__ void lds_load16(u32x4 desc, uint32_t off, uint32_t dst) {
-  if constexpr (STREAM)
+template <int W, bool STREAM> __device__ __forceinline__ void lds_load(u32x4 desc, uint32_t off, uint32_t dst) {
+  static_assert(W == 16 || W == 4, "width");
+  if constexpr (W == 4 && STREAM)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen nt lds"
+                 : : "s"(dst), "v"(off), "s"(desc) : "memory");
+  else if constexpr (W == 4)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 : : "s"(dst), "v"(off), "s"(desc) : "memory");
+  else if constexpr (STREAM)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
                  : : "s"(dst), "v"(off), "s"(desc) : "memory");
   else
@@ -388,20 +395,28 @@ template <DT D, bool TR> struct Cursor {
   }
 };
 
-template <DT D, bool TR, int R, int THREADS> struct Direct {
+// W: bytes a lane loads at once, 16 where rows start and end on 16 bytes, else (fp32) one
+// element's 4: four times the instructions, but at any address (3243 x 1963 -> 4216 in fp32:
+// 517 us, 701 with the chunks going through registers).
+template <DT D, bool TR, int R, int THREADS, int W> struct Direct {
   typedef Tile<D, TR, R, THREADS> T;
-  static constexpr int NI = T::NI;
-  static_assert(TR || THREADS / T::CPR % 8 == 0 || NI == 1, "every chunk of a thread has the same place in its row");
-  uint32_t off[NI];  // byte offset of this lane's chunks from the tile's first element
-  int kk;            // contraction index of chunk 0 inside the tile
+  static constexpr int PER = 16 / W;      // instructions that fill 1 KB
+  static constexpr int NL = T::NI * PER;  // loads of a thread
+  static_assert(TR || THREADS / T::CPR % 8 == 0 || T::NI == 1, "every chunk of a thread has the same place in its row");
+  static_assert(W == 16 || W == T::ES, "a load is a chunk or an element");
+  uint32_t off[NL];  // byte offset of this lane's loads from the tile's first element
+  int kk[PER];       // contraction index of the first PER loads inside the tile
   __device__ __forceinline__ void init(int64_t ld, int64_t r0, int64_t nr, int tid) {
+    const int lane = tid & 63;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int c = i * THREADS + tid, row = c / T::CPR, ch = swz<D, TR, T::CPR>(row, c % T::CPR);
-      const bool in = TR ? r0 + T::EPC * ch < nr : r0 + row < nr;
-      off[i] = in ? (uint32_t)(row * (int)ld + T::EPC * ch) * T::ES : OUTSIDE;
+    for (int i = 0; i < NL; ++i) {
+      const int c = i / PER * THREADS + (tid - lane) + (i % PER * 64 + lane) * W / 16;  // the chunk
+      const int row = c / T::CPR, ch = swz<D, TR, T::CPR>(row, c % T::CPR);
+      const int col = T::EPC * ch + (W == 16 ? 0 : lane & (PER - 1));
+      const bool in = TR ? r0 + col < nr : r0 + row < nr;
+      off[i] = in ? (uint32_t)(row * (int)ld + col) * T::ES : OUTSIDE;
+      if (i < PER) kk[i] = TR ? row : col;
     }
-    kk = TR ? tid / T::CPR : T::EPC * swz<D, TR, T::CPR>(tid / T::CPR, tid % T::CPR);
   }
   // The tile at p, k contraction indices of which exist, into LDS from byte address lds on
   // (this wave's part).
@@ -410,9 +425,9 @@ template <DT D, bool TR, int R, int THREADS> struct Direct {
   __device__ __forceinline__ void stage(const char* p, int k, uint32_t lds, int wave) const {
     const u32x4 r = raw_desc(p);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const uint32_t o = kk + (TR ? i * (THREADS / T::CPR) : 0) < k ? off[i] : OUTSIDE;
-      lds_load16<STREAM>(r, o, __builtin_amdgcn_readfirstlane(lds + (i * THREADS + wave * 64) * 16));
+    for (int i = 0; i < NL; ++i) {
+      const uint32_t o = kk[i % PER] + (TR ? i / PER * (THREADS / T::CPR) : 0) < k ? off[i] : OUTSIDE;
+      lds_load<W, STREAM>(r, o, __builtin_amdgcn_readfirstlane(lds + (i / PER * THREADS + wave * 64) * 16 + i % PER * 64 * W));
     }
   }
 };
@@ -436,7 +451,7 @@ __device__ __forceinline__ void lds_barrier() {
 // the product streams its weights: three or more buffers keep about 100 KB of loads in
 // flight per compute unit.
 template <DT D, bool PT, bool QT, bool DUAL, int BM, int BN, int NST, int WM, int WN, bool ALN>
-__global__ __launch_bounds__(64 * WM * WN) void k_product_ring(const Gemm a) {
+__global__ __launch_bounds__(64 * WM * WN, BM == 128 ? 2 : 1) void k_product_ring(const Gemm a) {
   constexpr int THREADS = 64 * WM * WN, NQ = DUAL ? 2 : 1;
   constexpr int PR = BM < 32 ? 32 : BM;  // staged rows of P: every thread has a chunk; those past M load nothing
   constexpr bool FEW = BM <= 64;
@@ -445,9 +460,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product_ring(const Gemm a) {
   typedef Tile<D, QT, BN / NQ, THREADS> TQ;
   constexpr int BK = TP::BK, KS = TP::KSTEP;
   typedef typename Frag<D>::type frag_t;
-  static_assert(ALN || NST == 2, "register staging uses two buffers");
+  constexpr bool DIRECT = ALN || D == DT::F32;  // loads write LDS themselves
+  constexpr int W = ALN ? 16 : 4;               // bytes of a direct load per lane
+  static_assert(DIRECT || NST == 2, "register staging uses two buffers");
   constexpr int STAGE = TP::BYTES + NQ * TQ::BYTES;
-  constexpr int LOADS = TP::NI + NQ * TQ::NI;  // of a wave, per step
   __shared__ __attribute__((aligned(1024))) unsigned char lds[NST * STAGE];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / WN, wn = wave % WN;
@@ -504,9 +520,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product_ring(const Gemm a) {
     }
   };
 
-  if constexpr (ALN) {
-    Direct<D, PT, PR, THREADS> dp;
-    Direct<D, QT, BN / NQ, THREADS> dq;
+  if constexpr (DIRECT) {
+    Direct<D, PT, PR, THREADS, W> dp;
+    Direct<D, QT, BN / NQ, THREADS, W> dq;
+    constexpr int LOADS = dp.NL + NQ * dq.NL;  // of a wave, per step
+    static_assert((NST - 2) * LOADS < 64, "the wait counts up to 63 loads");
     dp.init(a.ldp, m0, BM < PR ? min(a.M, m0 + BM) : a.M, tid);
     dq.init(a.ldq, n0, a.N, tid);
     Cursor<D, PT> cp;
@@ -541,7 +559,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_product_ring(const Gemm a) {
     }
     wait_loads<0>();  // LDS must not be given up with loads into it in flight
   } else {
-    // Any element-aligned operand: through registers, the next step's loads issued before
+    // 16-bit rows at any address: through registers, the next step's loads issued before
     // this step's matrix ops and written to the other buffer after them.
     uint4 vp[TP::NI], vq[NQ][TQ::NI];
     auto fetch = [&](int t) {
@@ -625,8 +643,8 @@ __global__ __launch_bounds__(512) void k_product_wide(const Gemm a) {
 
   const int kt = (a.K + BK - 1) / BK, steps = kt * a.segments;
   const int t0 = (int)((int64_t)steps * pl.split / pl.splits), t1 = (int)((int64_t)steps * (pl.split + 1) / pl.splits);
-  Direct<D, PT, 128, THREADS> dp[2];
-  Direct<D, QT, 256 / NQ, THREADS> dq;
+  Direct<D, PT, 128, THREADS, 16> dp[2];
+  Direct<D, QT, 256 / NQ, THREADS, 16> dq;
   dp[0].init(a.ldp, m0, a.M, tid);
   dp[1].init(a.ldp, m0 + 128, a.M, tid);
   dq.init(a.ldq, n0, a.N, tid);
@@ -803,7 +821,7 @@ constexpr Shape F64W{64, 256, 64, 256, 0.722, 0.735, 5.175, 0.544, 6.2};
 constexpr Shape F16{16, 64, 64, 768, 0.862, 0.400, 5.099, 0.083, 7.3};
 constexpr Shape F16D{16, 128, 64, 512, 1.310, 0.709, 1.857, 0.423, 3.1};
 constexpr Shape F16W{16, 256, 64, 256, 0.737, 0.626, 4.047, 0.419, 2.4};
-// Operands that are not 16-byte aligned, fp32, and both.
+// 16-bit operands that are not 16-byte aligned, and fp32.
 constexpr Shape U128{128, 128, 64, 512, 1.682, 1.934, 4.764, 0.518, 5.0};
 constexpr Shape U64{64, 64, 64, 1024, 1.908, 0.857, 4.768, 0.302, 6.7};
 constexpr Shape U64D{64, 128, 64, 768, 2.191, 1.832, 2.396, 0.705, 6.7};
@@ -814,11 +832,6 @@ constexpr Shape S64{64, 64, 32, 768, 1.859, 0.818, 4.282, 0.352, 9.4};
 constexpr Shape S64D{64, 128, 32, 512, 2.369, 1.428, 4.227, 0.696, 10.4};
 constexpr Shape S16{16, 64, 32, 768, 0.968, 0.378, 6.002, 0.093, 20.0};
 constexpr Shape S16D{16, 128, 32, 512, 1.163, 0.053, 5.300, 0.182, 20.0};
-constexpr Shape V128{128, 128, 32, 256, 3.058, 3.541, 3.581, 0.499, 4.5};
-constexpr Shape V64{64, 64, 32, 1024, 3.223, 1.271, 4.156, 0.336, 6.6};
-constexpr Shape V64D{64, 128, 32, 512, 3.248, 2.506, 1.765, 0.751, 7.9};
-constexpr Shape V16{16, 64, 32, 1024, 2.101, 0.910, 4.773, 0.109, 20.0};
-constexpr Shape V16D{16, 128, 32, 768, 2.923, 1.608, 3.016, 0.208, 20.0};
 
 static Plan make_plan(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch,
                       bool aln) {
@@ -829,9 +842,9 @@ static Plan make_plan(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, 
   };
   const bool f32 = dtype == HCLRMIX_F32, few = M <= 16 && !p_trans;
   if (f32 || !aln) {
-    consider(!f32 ? U128 : aln ? S128 : V128);
-    consider(!f32 ? (dual ? U64D : U64) : aln ? (dual ? S64D : S64) : (dual ? V64D : V64));
-    if (few) consider(!f32 ? (dual ? U16D : U16) : aln ? (dual ? S16D : S16) : (dual ? V16D : V16));
+    consider(f32 ? S128 : U128);
+    consider(f32 ? (dual ? S64D : S64) : (dual ? U64D : U64));
+    if (few) consider(f32 ? (dual ? S16D : S16) : (dual ? U16D : U16));
   } else {
     consider(MID);
     consider(WIDE);
@@ -855,28 +868,31 @@ size_t product_scratch(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans,
   return most;
 }
 
-// k_product_ring for one tile shape.
-template <DT D, bool PT, bool QT, bool DUAL, int BM, int BN, int NST, int WM, int WN, bool ALN>
-static hipError_t ring(const Gemm& g, unsigned n, hipStream_t s) {
-  return launch(nullptr, k_product_ring<D, PT, QT, DUAL, BM, BN, NST, WM, WN, ALN>, dim3(n), dim3(64 * WM * WN), 0, s, g);
+// k_product_ring for one tile shape; rows staged through registers take two buffers.
+template <DT D, bool PT, bool QT, bool DUAL, int BM, int BN, int NST, int WM, int WN>
+static hipError_t ring(const Gemm& g, bool aln, unsigned n, hipStream_t s) {
+  constexpr int ODD = D == DT::F32 ? NST : 2;
+  return launch(nullptr, aln ? k_product_ring<D, PT, QT, DUAL, BM, BN, NST, WM, WN, true> : k_product_ring<D, PT, QT, DUAL, BM, BN, ODD, WM, WN, false>,
+                dim3(n), dim3(64 * WM * WN), 0, s, g);
 }
 
 template <DT D, bool PT, bool QT, bool DUAL>
 static hipError_t go(const Gemm& g, const Shape& sh, bool aln, unsigned n, hipStream_t s) {
   constexpr int BN = DUAL ? 128 : 64;
-  if constexpr (!PT) {
-    if (sh.bm == 16 && !aln) return ring<D, PT, QT, DUAL, 16, BN, 2, 1, 4, false>(g, n, s);
-    if constexpr (D != DT::F32) {
-      if (sh.bm == 16 && sh.bn == 256) return ring<D, PT, QT, DUAL, 16, 256, 3, 1, 4, true>(g, n, s);
-      if (sh.bm == 64 && sh.bn == 256) return ring<D, PT, QT, DUAL, 64, 256, 3, 1, 4, true>(g, n, s);
-    }
-    if (sh.bm == 16) return ring<D, PT, QT, DUAL, 16, BN, DUAL ? 3 : 4, 1, 4, true>(g, n, s);
-  }
-  if (sh.bm == 64) return aln ? ring<D, PT, QT, DUAL, 64, BN, 3, 2, 2, true>(g, n, s) : ring<D, PT, QT, DUAL, 64, BN, 2, 2, 2, false>(g, n, s);
-  if constexpr (D != DT::F32) {
+  if constexpr (D != DT::F32) {  // aligned operands only
     if (sh.bm == 256) return launch(nullptr, k_product_wide<D, PT, QT, DUAL>, dim3(n), dim3(512), 0, s, g);
+    if constexpr (!PT) {
+      if (sh.bm == 16 && sh.bn == 256)
+        return launch(nullptr, k_product_ring<D, PT, QT, DUAL, 16, 256, 3, 1, 4, true>, dim3(n), dim3(256), 0, s, g);
+      if (sh.bm == 64 && sh.bn == 256)
+        return launch(nullptr, k_product_ring<D, PT, QT, DUAL, 64, 256, 3, 1, 4, true>, dim3(n), dim3(256), 0, s, g);
+    }
   }
-  return aln ? ring<D, PT, QT, DUAL, 128, 128, 2, 2, 2, true>(g, n, s) : ring<D, PT, QT, DUAL, 128, 128, 2, 2, 2, false>(g, n, s);
+  if constexpr (!PT) {
+    if (sh.bm == 16) return ring<D, PT, QT, DUAL, 16, BN, DUAL ? 3 : 4, 1, 4>(g, aln, n, s);
+  }
+  if (sh.bm == 64) return ring<D, PT, QT, DUAL, 64, BN, 3, 2, 2>(g, aln, n, s);
+  return ring<D, PT, QT, DUAL, 128, 128, 2, 2, 2>(g, aln, n, s);
 }
 
 template <DT D> static hipError_t go_layout(const Product& p, const Gemm& g, const Shape& sh, bool aln, unsigned n, hipStream_t s) {
