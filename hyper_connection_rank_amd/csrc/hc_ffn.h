@@ -83,7 +83,7 @@ template <DT D, int N> __device__ __forceinline__ void act_slope_n(int kind, flo
     case ACT_RELU:
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        d[e] = x[e] > 0.0f ? 1.0f : 0.0f;
+        d[e] = x[e] > 0.0f ? 1.0f : (x[e] <= 0.0f ? 0.0f : x[e]);  // NaN stays NaN
         x[e] = relu(x[e]);
       }
       break;
@@ -108,7 +108,8 @@ template <DT D, int N> __device__ __forceinline__ void act_slope_n(int kind, flo
 #pragma unroll
       for (int e = 0; e < N; ++e) {  // 1 - tanh(t)^2 = 4 s (1 - s) with s = sigmoid(2 t)
         const float s = sigmoid_of<D>(gelu_arg(x[e]));
-        d[e] = s + 2.0f * x[e] * s * (1.0f - s) * GELU_C * (1.0f + 3.0f * GELU_A * x[e] * x[e]);
+        const float c = __builtin_amdgcn_fmed3f(x[e], -32.0f, 32.0f);  // beyond, s (1 - s) is 0 and x^3 may be infinite
+        d[e] = s + 2.0f * c * s * (1.0f - s) * GELU_C * (1.0f + 3.0f * GELU_A * c * c);
         x[e] = x[e] * s;
       }
       break;
@@ -129,9 +130,8 @@ template <DT D, int N> __device__ __forceinline__ void act_slope_n(int kind, flo
 
 // ------------------------------------------------------------------ element access
 
-// Four and eight elements from any element-aligned address, n of them valid
-// (the others read as 0). ALN: every address is 16-byte aligned (four 16-bit
-// elements: 8-byte) and n is always the full count.
+// Eight elements from any element-aligned address, n of them valid (the others
+// read as 0). ALN: every address is 16-byte aligned and n is always at least 8.
 typedef unsigned u32x4_h __attribute__((ext_vector_type(4), aligned(2)));
 typedef unsigned u32x4_w __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -181,28 +181,24 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
 }
 
 // Eight elements as they are stored (half the registers of their fp32 values for 16-bit T).
-// Aligned loads are non-temporal: rows are read once.
 template <DT D> struct Raw8 {
   u32x4 v;
 };
 template <> struct Raw8<DT::F32> {
   u32x4 v, w;
 };
-template <DT D, bool ALN> __device__ __forceinline__ Raw8<D> load_raw8(const void* base, int64_t i, int n) {
+// From any element-aligned address, n of them valid.
+template <DT D> __device__ __forceinline__ Raw8<D> load_raw8(const void* base, int64_t i, int n) {
   Raw8<D> r;
-  if constexpr (ALN) {
-    const u32x4* p = (const u32x4*)((const typename Store<D>::type*)base + i);
-    r.v = __builtin_nontemporal_load(p);
-    if constexpr (D == DT::F32) r.w = __builtin_nontemporal_load(p + 1);
-  } else if constexpr (D == DT::F32) {
+  if constexpr (D == DT::F32) {
     float x[8];
-    load8<D, ALN>(base, i, n, x);
+    load8<D, false>(base, i, n, x);
     r.v = __builtin_bit_cast(u32x4, f32x4{x[0], x[1], x[2], x[3]});
     r.w = __builtin_bit_cast(u32x4, f32x4{x[4], x[5], x[6], x[7]});
   } else {
     const uint16_t* p = (const uint16_t*)base + i;
     if (n >= 8) {
-      r.v = to_u32x4(ld16<D, ALN>(p));
+      r.v = to_u32x4(ld16<D, false>(p));
     } else {
       uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -285,7 +281,6 @@ hipError_t launch_column_sums(const float* partial, int nrows, int64_t pitch, in
 // One product out[m][n] = epilogue(sum over k of P(m, k) Q(k, n)) or a pair of
 // them. P(m, k) is p[m * ldp + k], or p[k * ldp + m] with p_trans; Q(k, n) is
 // q[k * ldq + n], or q[n * ldq + k] with q_trans.
-//   pairs = 1: one product.
 //   segments = 2: out = P0 Q0 + P1 Q1 (one sum over both contractions).
 //   batch = 2: two products out[b] = P_b Q_b in one launch.
 //   dual: g = P0 Q0 + bias0, u = P0 Q1 + bias1, out[0] = act(g) * u.

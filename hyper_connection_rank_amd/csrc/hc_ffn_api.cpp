@@ -182,18 +182,17 @@ hclrmix_status size_of(const hclrmix_product* p, size_t* bytes, bool glu, bool b
   return ok();
 }
 
-hc::Product base_product(const hclrmix_product* p) {
+hc::Product base_product() {
   hc::Product r{};
   r.segments = r.batch = 1;
   r.act = hc::ACT_NONE;
-  (void)p;
   return r;
 }
 
 // dx = dz0 w0^T (+ dz1 w1^T).
 hc::Product dx_product(const hclrmix_product* p, const Strides& s, const void* dz0, const void* dz1, const void* w0,
                        const void* w1, void* dx) {
-  hc::Product r = base_product(p);
+  hc::Product r = base_product();
   r.p[0] = dz0;
   r.p[1] = dz1;
   r.q[0] = w0;
@@ -211,7 +210,7 @@ hc::Product dx_product(const hclrmix_product* p, const Strides& s, const void* d
 // dw_b = x^T dz_b.
 hc::Product dw_product(const hclrmix_product* p, const Strides& s, const void* x, const void* dz0, const void* dz1,
                        void* dw0, void* dw1) {
-  hc::Product r = base_product(p);
+  hc::Product r = base_product();
   r.p[0] = x;
   r.p[1] = dz1 ? x : nullptr;
   r.q[0] = dz0;
@@ -348,7 +347,7 @@ hclrmix_status hclrmix_linear(const void* x, const void* weight, const void* bia
           es))
     return st;
   if (hclrmix_status st = check_workspace(workspace, workspace_bytes, w.bytes)) return st;
-  hc::Product r = base_product(problem);
+  hc::Product r = base_product();
   r.p[0] = x;
   r.q[0] = weight;
   r.ldp = st_.x;
@@ -391,7 +390,7 @@ hclrmix_status hclrmix_glu(const void* x, const void* gate_weight, const void* u
           es))
     return st;
   if (hclrmix_status st = check_workspace(workspace, workspace_bytes, w.bytes)) return st;
-  hc::Product r = base_product(problem);
+  hc::Product r = base_product();
   r.p[0] = x;
   r.q[0] = gate_weight;
   r.q[1] = up_weight;

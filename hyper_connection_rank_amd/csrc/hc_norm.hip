@@ -77,7 +77,7 @@ template <DT D, bool ALN, int NV> struct RowChunks {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int h = 8 * (t + stride * i);
-        c[i] = base && live && h < H ? load_raw8<D, ALN>(base, row + h, H - h) : zero_raw8<D>();
+        c[i] = base && live && h < H ? load_raw8<D>(base, row + h, H - h) : zero_raw8<D>();
       }
     }
   }
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(ONE ? 256 : 64 * WAVES) void k_norm_bwd(const NormA
     r.renew();
     n.renew();
     const float rr = rinv_rms(s[0], inv_h, a.eps);
-    const float cr = rr * rr * rr * (s[1] * inv_h);
+    const float cr = rr * (rr * (rr * (s[1] * inv_h)));  // in this order rr^3 of tiny or huge rows stays in range
     const float ry = a.post_norm ? rinv_rms(s[2], inv_h, a.eps) : 1.0f;
     const float cp = coef * ry;
     float u = 0.0f;  // p y
@@ -346,13 +346,13 @@ __global__ __launch_bounds__(ONE ? 256 : 64 * WAVES) void k_norm_bwd(const NormA
     row_sums<ONE, 1>(&u, red[parity] + 3 * MAX_WAVES, pl.W, pl.wave, pl.lane);
     y.renew();
     if (!GE && a.d_gate && t == 0) st<D>(a.d_gate, m, a.alpha * ry * u);
-    const float cy = a.post_norm ? cp * ry * ry * (u * inv_h) : 0.0f;
+    const float cy = a.post_norm ? ry * (ry * (u * inv_h)) : 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float yv[8];
       unpack_raw8<D>(y.c[i], yv);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[i][e] = fmaf(-yv[e], cy, cp * q[i][e]);
+      for (int e = 0; e < 8; ++e) q[i][e] = cp * fmaf(-yv[e], cy, q[i][e]);
     }
     store_row<D, ALN, NV>(a.dy, row, H, t, S, q);
     if constexpr (AHEAD) {

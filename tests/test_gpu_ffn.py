@@ -6,6 +6,8 @@ captured graphs, side streams, shared workspaces, and the operators in a row
 as a model uses them between two hyper-connection blocks."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -530,3 +532,55 @@ def test_product_gradients_by_differences():
                 # 120 elements with independent signs; fp32 noise of f over 2 e
                 tol = 4 * e * e * 120 ** 0.5 + 2.0 ** -22 * 120 ** 0.5 / e + 1e-3 * abs(ana)
                 assert abs(num - ana) <= tol, (act, name, num, ana, tol)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -50, 2.0 ** 40])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hidden", [77, 520, 4104])
+def test_norm_backward_of_tiny_and_huge_rows(hidden, dtype, scale):
+    """No epsilon: 1 / rms^3 of such rows leaves fp32's range, the gradients do not."""
+    dt = T_OF[dtype]
+    y, r = rand((5, hidden), dt, 1, scale), rand((5, hidden), dt, 2, scale)
+    dr, dn = None, rand((5, hidden), dt, 4)
+    post, pre = rand((hidden,), dt, 5), rand((hidden,), dt, 6)
+    got = hc.residual_norm_backward(y, r, dr, dn, post_scale=post, pre_scale=pre, alpha=0.5, epsilon=0.0)
+    ref = R.norm_backward(y, r, dr, dn, None, post, pre, True, 0.5, 0.0)
+    for g, name in zip(got, NAMES):
+        if g is not None:
+            within(g, *ref[name], name)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_slopes_of_extreme_preactivations(dtype, act):
+    """The type's largest and lowest values, and others whose square or cube is infinite in fp32."""
+    dt = T_OF[dtype]
+    m, k, n = 3, 24, 16
+    top = torch.finfo(dt).max
+    big = [0.0, -0.0, top, -top, top / 4, -top / 4, 40.0, -40.0, 300.0, -300.0] + ([] if dtype == "f16" else [1e20, -1e20, 1e13, -1e13])
+    x, w, dy = rand((m, k), dt, 1), rand((k, n), dt, 2), rand((m, n), dt, 3)
+    p = rand((m, n), dt, 4)
+    p[1, :len(big)] = torch.tensor(big, dtype=torch.float64).to(dt)
+    got = dict(zip(("dx", "dw0", "db0"), hc.linear_backward(x, w, dy, p, activation=act, bias=True)))
+    ref = R.linear_backward(x, w, dy, p, act)
+    for name, g in got.items():
+        within(g, *ref[name], name)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_nan_preactivation_reaches_its_gradients_only(dtype, act):
+    dt = T_OF[dtype]
+    m, k, n = 5, 24, 16
+    x, w, wu, dy = rand((m, k), dt, 1), rand((k, n), dt, 2), rand((k, n), dt, 5), rand((m, n), dt, 3)
+    p, u = rand((m, n), dt, 4), rand((m, n), dt, 6)
+    p[2, 7] = math.nan
+    rows, cols = torch.arange(m, device="cuda") == 2, torch.arange(n, device="cuda") == 7
+    dx, dw, db = hc.linear_backward(x, w, dy, p, activation=act, bias=True)
+    gx, gg, gu, bg, bu = hc.glu_backward(x, w, wu, p, u, dy, activation=act, bias=True)
+    for d in (dx, gx):
+        assert torch.equal(d.isnan(), rows[:, None].expand(m, k))
+    for d in (dw, gg, gu):
+        assert torch.equal(d.isnan(), cols[None].expand(k, n))
+    for d in (db, bg, bu):
+        assert torch.equal(d.isnan(), cols)
