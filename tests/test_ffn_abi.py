@@ -164,7 +164,7 @@ def test_norm_alignment(name):
 def test_norm_workspace():
     c = norm(True)
     need = hc.hclrmix_residual_norm_workspace_size(c.problem)
-    assert need >= 4096 + 4 * 2 * 64 * 4
+    assert need >= 4096 + 2 * 64 * 4  # the counters and, for up to 4 rows, one workgroup's two rows of fp32 sums
     c.ws_bytes = need - 1
     _expect(c, W, str(need))
     c = norm(True, workspace=None)
