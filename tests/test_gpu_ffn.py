@@ -424,10 +424,10 @@ def test_captured_graphs_replay(dtype):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             outs = step(xs, ws)
-        graphs.append((g, xs, outs))
+        graphs.append((g, xs, outs, ws))  # a graph's buffers live as long as it does
     eager_ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
     for k in range(4):
-        g, xs, outs = graphs[k % 2]
+        g, xs, outs, _ = graphs[k % 2]
         new = rand((5, 2560), dt, 50 + k)
         xs.copy_(new)
         g.replay()
