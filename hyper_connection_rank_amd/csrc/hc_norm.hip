@@ -74,7 +74,7 @@ template <DT D, bool ALN, int NV> struct RowChunks {
       for (int i = 0; i < NV; ++i) {
         const int o = 8 * ES * (t + stride * i);
         c[i].v = __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 2);  // non-temporal: read once
-        if constexpr (D == DT::F32) c[i].w = __builtin_amdgcn_raw_buffer_load_b128(r, o, 16, 2);
+        if constexpr (D == DT::F32) c[i].w = __builtin_amdgcn_raw_buffer_load_b128(r, o + 16, 0, 2);
       }
     } else {
 #pragma unroll
@@ -116,7 +116,7 @@ __device__ __forceinline__ void store_row(void* base, int64_t row, int H, int t,
       const int o = 8 * ES * (t + stride * i);
       if constexpr (D == DT::F32) {
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{x[i][0], x[i][1], x[i][2], x[i][3]}), r, o, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{x[i][4], x[i][5], x[i][6], x[i][7]}), r, o, 16, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{x[i][4], x[i][5], x[i][6], x[i][7]}), r, o + 16, 0, 0);
       } else {
         __builtin_amdgcn_raw_buffer_store_b128(to_u32x4(pack8<D>(x[i])), r, o, 0, 0);
       }
