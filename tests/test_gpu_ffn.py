@@ -584,3 +584,106 @@ def test_nan_preactivation_reaches_its_gradients_only(dtype, act):
         assert torch.equal(d.isnan(), cols[None].expand(k, n))
     for d in (db, bg, bu):
         assert torch.equal(d.isnan(), cols)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each stream with a workspace of its own: the bits of calls alone."""
+    x, w, b, _ = linear_inputs(8, 4096, 320, torch.bfloat16, 3)
+    wu = rand((4096, 320), torch.bfloat16, 4, 4096 ** -0.5)
+    dy = rand((8, 320), torch.bfloat16, 5)
+    size = 32 << 20
+
+    def step(ws):
+        h, g, u = hc.glu(x, w, wu, save=True, workspace=ws)
+        return (h,) + hc.glu_backward(x, w, wu, g, u, dy, bias=True, workspace=ws)[:3] + (hc.linear(x, w, b, workspace=ws),)
+
+    ref = step(torch.zeros(size, dtype=torch.uint8, device="cuda"))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for s, ws in zip(streams, spaces):
+            with torch.cuda.stream(s):
+                got.append(step(ws))
+    torch.cuda.synchronize()
+    for g in got:
+        same(g, ref, "two streams")
+
+
+def test_the_same_tensor_as_several_inputs():
+    dt = torch.bfloat16
+    x, w = rand((33, 72), dt, 1), rand((72, 72), dt, 2, 72 ** -0.5)
+    s = rand((72,), dt, 3)
+    y = hc.linear(x, w, s, x, activation="silu")
+    within(y, *R.linear(x, w, s, x, "silu")[:2], "y")
+    h = hc.glu(x, w, w, s, s)
+    within(h, *R.glu(x, w, w, s, s, "silu")["h"], "h")
+    ref = R.norm(x, x, x, s, s, True, 1.0, 1e-5)
+    for got, name in zip(hc.residual_norm(x, x, gate=x, post_scale=s, pre_scale=s), ("residual_out", "normed")):
+        within(got, *ref[name], name)
+
+
+def test_tensors_beyond_4_gib():
+    """Rows, outputs and weights whose byte and element offsets pass 32 bits, at their ends."""
+    dt = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(11)
+
+    def big(*shape, std=1.0):
+        return torch.randn(*shape, generator=gen, device="cuda", dtype=dt) * std
+
+    # norms: 270,000 rows of 8,200
+    rows, h = 270000, 8200
+    y, res, gate, s = big(rows, h), big(rows, h), big(rows), 1 + big(h, std=0.1)
+    assert y.numel() * 2 > 1 << 32
+    pick = torch.tensor([0, 261902, 261903, 261904, rows - 1], device="cuda")
+    at = lambda t: t.index_select(0, pick)  # noqa: E731
+    r, n = hc.residual_norm(y, res, gate=gate, post_scale=s, pre_scale=s)
+    ref = R.norm(at(y), at(res), at(gate), s, s, True, 1.0, 1e-5)
+    within(at(r), *ref["residual_out"], "residual_out")
+    within(at(n), *ref["normed"], "normed")
+    dy, dr, dg, _, _ = hc.residual_norm_backward(y, r, res, n, gate=gate, post_scale=s, pre_scale=s)
+    ref = R.norm_backward(at(y), at(r), at(res), at(n), at(gate), s, s, True, 1.0, 1e-5)
+    for got, name in zip((dy, dr, dg), NAMES):
+        within(at(got), *ref[name], name)
+    del y, res, r, n, dy, dr
+    # many rows in, out and as the contraction of the weight's gradient
+    rows, k, n_ = 1050000, 2056, 24
+    x, w, b = big(rows, k), big(k, n_, std=k ** -0.5), big(n_)
+    assert x.numel() * 2 > 1 << 32
+    pick = torch.tensor([0, 1044481, 1044494, rows - 1], device="cuda")
+    y = hc.linear(x, w, b)
+    within(at(y), *R.linear(at(x), w, b, None, "none")[:2], "y")
+    dx, dw, db = hc.linear_backward(x, w, y, bias=True)
+    within(at(dx), *R.linear_backward(at(x), w, at(y), None, "none")["dx"], "dx")
+    exact = torch.zeros(k, n_, dtype=torch.float64, device="cuda")
+    square = exact.clone()
+    for i in range(0, rows, 65536):
+        a, c = x[i:i + 65536].double(), y[i:i + 65536].double()
+        exact += a.t().contiguous() @ c
+        square += (a * a).t().contiguous() @ (c * c)
+    # fp32 sums of `rows` products, as in R.product
+    within(dw, exact, 8 * R.F * rows ** 0.5 * (square.sqrt() + exact.abs()), "dw")
+    yd = y.double()
+    within(db, yd.sum(0), (rows / 128 / 4 + 128 + 16) * R.F * yd.abs().sum(0), "db")
+    del yd, dx
+    wide = rand((n_, k), dt, 12, n_ ** -0.5)
+    hh, g, u = hc.glu(y, wide, wide, save=True)
+    ref = R.glu(at(y), wide, wide, None, None, "silu")
+    for got, name in zip((hh, g, u), ("h", "g", "u")):
+        within(at(got), *ref[name], name)
+    del x, y, hh, g, u
+    # a weight of 2^32 - 2^19 elements
+    k, n_ = 65528, 65536
+    x, w = big(2, k), big(k, n_, std=k ** -0.5)
+    y = hc.linear(x, w)
+    cols = torch.tensor([0, 1, 32767, 65535], device="cuda")
+    within(y.index_select(1, cols), *R.linear(x, w.index_select(1, cols), None, None, "none")[:2], "y of a wide weight")
+    dy = big(2, n_)
+    dx, dw, _ = hc.linear_backward(x, w, dy)
+    pick = torch.tensor([0, 32767, 32768, k - 1], device="cuda")
+    ref = R.linear_backward(x.index_select(1, pick), at(w), dy, None, "none")
+    within(dx.index_select(1, pick), *ref["dx"], "dx of a wide weight")
+    within(at(dw), *ref["dw0"], "dw of a wide weight")
+    del x, w, y, dx, dw
+    torch.cuda.empty_cache()
