@@ -117,8 +117,10 @@ def _product_grads(x, branches, dt):
         rw, bw = product(xd.t(), dz)
         bw = bw + xd.abs().t() @ e
         if rounded and dt != torch.float32:
-            ex = ex + 4 * U(dt) * torch.sqrt((dz * dz) @ (wd * wd).t())
-            bw = bw + 4 * U(dt) * torch.sqrt((xd * xd).t() @ (dz * dz))
+            # dz rounded to T is off by at most U |dz|, or half a step of T's subnormal numbers where that is
+            # more (fp16, |dz| < 2^-14: 2^-25); the latter's sum is at most 2^-25 times the factors' absolute sum
+            ex = ex + 4 * U(dt) * torch.sqrt((dz * dz) @ (wd * wd).t()) + tiny(dt) * wd.abs().sum(1)
+            bw = bw + 4 * U(dt) * torch.sqrt((xd * xd).t() @ (dz * dz)) + tiny(dt) * xd.abs().sum(0)[:, None]
         n = dz.shape[0] / 64 + 64 + 16
         out[f"dw{i}"] = (rw, bw)
         out[f"db{i}"] = (dz.sum(0), n * F * dz.abs().sum(0) + e.sum(0))

@@ -687,3 +687,45 @@ def test_tensors_beyond_4_gib():
     within(at(dw), *ref["dw0"], "dw of a wide weight")
     del x, w, y, dx, dw
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("gate", ["row", "element"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,H", [(6, 6152), (530, 4104), (5, 5001)])
+def test_norm_backward_of_two_chunks_a_thread(rows, H, dtype, gate):
+    t = norm_inputs(rows, H, T_OF[dtype], gate, 7 + rows + H)
+    dres, dn = rand((rows, H), T_OF[dtype], 5), rand((rows, H), T_OF[dtype], 6)
+    ref = R.norm_backward(t["y"], t["residual"], dres, dn, t["gate"], t["post_scale"], t["pre_scale"], True, 0.5, 1e-6)
+    for got, name in zip(_norm_back(t, t["residual"], dres, dn), NAMES):
+        within(got, *ref[name], (name, rows, H, dtype, gate))
+
+
+# Sizes that between them take every tile shape of every operand layout, whole and split, aligned and not.
+TILE_SHAPES_16 = [(1, 776, 8200), (1, 2568, 8200), (1, 8200, 2568), (33, 4104, 200), (130, 520, 8200), (200, 200, 8200),
+                  (200, 2568, 8200), (200, 8200, 2568), (200, 2056, 4104), (200, 4104, 2056), (257, 200, 10248),
+                  (1025, 200, 8200), (1025, 8200, 200), (1025, 1544, 5128), (130, 10248, 8200), (33, 2569, 201),
+                  (257, 201, 10249), (200, 1545, 4105), (200, 1545, 5129), (1025, 321, 4105), (1025, 4105, 201),
+                  (16, 10249, 201), (200, 4105, 1545)]
+TILE_SHAPES_32 = [(200, 521, 4105), (200, 201, 10249), (1025, 201, 4105), (257, 10249, 201), (200, 4105, 1033),
+                  (200, 1033, 4105), (16, 8201, 201), (200, 520, 4104), (200, 200, 10248), (1025, 200, 4104), (200, 1032, 4104),
+                  (257, 10248, 200), (200, 4104, 1032), (16, 8200, 200)]
+
+
+@pytest.mark.parametrize("shape,dtype", [(s, d) for d in ("bf16", "f16") for s in TILE_SHAPES_16] + [(s, "f32") for s in TILE_SHAPES_32])
+def test_every_tile_shape(shape, dtype):
+    m, k, n = shape
+    dt = T_OF[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(m + k + n)
+    draw = lambda *s, std=1.0: (torch.randn(*s, generator=gen, device="cuda") * std).to(dt)  # noqa: E731
+    x, w, wu, b, res = draw(m, k), draw(k, n, std=k ** -0.5), draw(k, n, std=k ** -0.5), draw(n), draw(m, n)
+    g, u, dy = draw(m, n), draw(m, n), draw(m, n)
+    within(hc.linear(x, w, b, res, activation="silu"), *R.linear(x, w, b, res, "silu")[:2], ("linear", shape, dtype))
+    ref = R.glu(x, w, wu, b, None, "gelu")
+    for got, name in zip(hc.glu(x, w, wu, b, None, activation="gelu", save=True), ("h", "g", "u")):
+        within(got, *ref[name], ("glu", name, shape, dtype))
+    ref = R.linear_backward(x, w, dy, g, "sigmoid")
+    for got, name in zip(hc.linear_backward(x, w, dy, g, activation="sigmoid", bias=True), ("dx", "dw0", "db0")):
+        within(got, *ref[name], ("linear_backward", name, shape, dtype))
+    ref = R.glu_backward(x, w, wu, g, u, dy, "silu")
+    for got, name in zip(hc.glu_backward(x, w, wu, g, u, dy, bias=True), GLU_NAMES):
+        within(got, *ref[name], ("glu_backward", name, shape, dtype))
