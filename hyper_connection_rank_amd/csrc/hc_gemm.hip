@@ -87,7 +87,7 @@ template <DT D, bool TR, int R, int THREADS> struct Tile {
   typedef typename Store<D>::type elem_t;
 
   // Reads this thread's chunks of the tile at output index r0 and contraction
-  // index k0 of an operand with nr output indices and K contraction indices, at any
+  // index k0 of a 16-bit operand with nr output indices and K contraction indices, at any
   // element-aligned address.
   static __device__ __forceinline__ void fetch(const void* base, int64_t ld, int64_t r0, int64_t nr, int k0, int K,
                                                int tid, uint4* v) {
@@ -107,10 +107,7 @@ template <DT D, bool TR, int R, int THREADS> struct Tile {
           uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
           for (int e = 0; e < EPC - 1; ++e)
-            if (e < left) {
-              if constexpr (D == DT::F32) w[e] = __float_as_uint(src[e]);
-              else w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
-            }
+            if (e < left) w[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
           v[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
