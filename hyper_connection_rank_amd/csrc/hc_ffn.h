@@ -27,16 +27,21 @@ constexpr float RSQRT2PI = 0.3989422804014327f;
 __device__ __forceinline__ float sigmoid_fast(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
 }
-// Phi(x), the normal distribution function, for the same use: Abramowitz and Stegun
-// 7.1.26 for erfc of |x| / sqrt 2 (absolute error below 1.5e-7).
+// Phi(x), the normal distribution function, for the same use. Phi(-a) = exp(-a^2 / 2) m(a) for
+// a >= 0, with m(a) = t P(t), t = 1 / (1 + 0.36 a): P has degree 6 and was fitted so that the
+// largest relative error over 0 <= a <= 15 is least (1.1e-6). With the fp32 steps' rounding the
+// relative error is below 2.2e-6 for |x| < 6 and 7e-6 beyond (the exponent's own rounding), far
+// below half a step of fp16 (4.9e-4) down to where the result leaves the normal numbers of T.
 __device__ __forceinline__ float phi_fast(float x) {
-  const float y = fabsf(x) * RSQRT2;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, y, 1.0f));
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  const float tail = 0.5f * p * t * __builtin_amdgcn_exp2f(y * y * -1.4426950408889634f);
+  const float a = fabsf(x);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.36f, a, 1.0f));
+  float p = fmaf(0.04649430513381958f, t, -0.17784516513347626f);
+  p = fmaf(p, t, 0.17835372686386108f);
+  p = fmaf(p, t, 0.02832658961415291f);
+  p = fmaf(p, t, 0.13907690346240997f);
+  p = fmaf(p, t, 0.14188815653324127f);
+  p = fmaf(p, t, 0.14370496571063995f);
+  const float tail = p * t * __builtin_amdgcn_exp2f(a * a * -0.7213475204444817f);
   return x < 0.0f ? tail : 1.0f - tail;
 }
 template <DT D> __device__ __forceinline__ float sigmoid_of(float x) {
@@ -48,9 +53,10 @@ template <DT D> __device__ __forceinline__ float phi_of(float x) {
 __device__ __forceinline__ float relu(float x) { return x > 0.0f ? x : (x <= 0.0f ? 0.0f : x); }  // NaN stays NaN
 __device__ __forceinline__ float gelu_arg(float x) { return 2.0f * GELU_C * (x + GELU_A * x * x * x); }
 
-// N values x replaced by act(x), for outputs of type D. GELU as x * erfc(-x / sqrt 2) / 2
-// and GELU_TANH as x * sigmoid(2 t), which equal the usual forms and keep their accuracy
-// for negative x, where 1 + erf and 1 + tanh cancel.
+// N values x replaced by act(x), for outputs of type D. GELU as x * Phi(x) with Phi's tail
+// computed as such (fp32: erfc(-x / sqrt 2) / 2, whose relative error grows as x^2 2^-24 with its
+// argument's rounding; 16 bits: phi_fast) and GELU_TANH as x * sigmoid(2 t): they equal the usual
+// forms and keep their relative accuracy for negative x, where 1 + erf and 1 + tanh cancel.
 template <DT D, int N> __device__ __forceinline__ void act_n(int kind, float* x) {
   switch (kind) {
     case ACT_RELU:
