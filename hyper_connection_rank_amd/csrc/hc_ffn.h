@@ -50,6 +50,17 @@ template <DT D> __device__ __forceinline__ float sigmoid_of(float x) {
 template <DT D> __device__ __forceinline__ float phi_of(float x) {
   return D == DT::F32 ? 0.5f * erfcf(-x * RSQRT2) : phi_fast(x);
 }
+// s = sigmoid(x) and c = 1 - s, both with their full relative accuracy (a subtraction from one
+// would leave c, and so the slope s c, few correct bits for large x): with e = exp(-|x|) they are
+// 1 / (1 + e) and e / (1 + e).
+template <DT D> __device__ __forceinline__ void sigmoid_both(float x, float& s, float& c) {
+  const float a = fabsf(x);
+  const float e = D == DT::F32 ? expf(-a) : __builtin_amdgcn_exp2f(a * -1.4426950408889634f);
+  const float r = D == DT::F32 ? 1.0f / (1.0f + e) : __builtin_amdgcn_rcpf(1.0f + e);
+  const float q = e * r;
+  s = x < 0.0f ? q : r;
+  c = x < 0.0f ? r : q;
+}
 __device__ __forceinline__ float relu(float x) { return x > 0.0f ? x : (x <= 0.0f ? 0.0f : x); }  // NaN stays NaN
 __device__ __forceinline__ float gelu_arg(float x) { return 2.0f * GELU_C * (x + GELU_A * x * x * x); }
 
@@ -96,8 +107,9 @@ template <DT D, int N> __device__ __forceinline__ void act_slope_n(int kind, flo
     case ACT_SILU:
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float s = sigmoid_of<D>(x[e]);
-        d[e] = s * (1.0f + x[e] * (1.0f - s));
+        float s, c;
+        sigmoid_both<D>(x[e], s, c);
+        d[e] = s * (1.0f + x[e] * c);
         x[e] = x[e] * s;
       }
       break;
@@ -113,17 +125,19 @@ template <DT D, int N> __device__ __forceinline__ void act_slope_n(int kind, flo
     case ACT_GELU_TANH:
 #pragma unroll
       for (int e = 0; e < N; ++e) {  // 1 - tanh(t)^2 = 4 s (1 - s) with s = sigmoid(2 t)
-        const float s = sigmoid_of<D>(gelu_arg(x[e]));
-        const float c = __builtin_amdgcn_fmed3f(x[e], -32.0f, 32.0f);  // beyond, s (1 - s) is 0 and x^3 may be infinite
-        d[e] = s + 2.0f * c * s * (1.0f - s) * GELU_C * (1.0f + 3.0f * GELU_A * c * c);
+        float s, c;
+        sigmoid_both<D>(gelu_arg(x[e]), s, c);
+        const float v = __builtin_amdgcn_fmed3f(x[e], -32.0f, 32.0f);  // beyond, s c is 0 and x^3 may be infinite
+        d[e] = s + 2.0f * v * s * c * GELU_C * (1.0f + 3.0f * GELU_A * v * v);
         x[e] = x[e] * s;
       }
       break;
     case ACT_SIGMOID:
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float s = sigmoid_of<D>(x[e]);
-        d[e] = s * (1.0f - s);
+        float s, c;
+        sigmoid_both<D>(x[e], s, c);
+        d[e] = s * c;
         x[e] = s;
       }
       break;

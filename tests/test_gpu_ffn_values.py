@@ -57,3 +57,43 @@ def test_gelu_keeps_its_relative_accuracy_in_the_tail(dtype):
     slope = 0.5 * torch.special.erfc(-xd * 0.5 ** 0.5) + xd * torch.exp(-0.5 * xd * xd) / (2 * math.pi) ** 0.5
     # two roundings: dz to T, then dx (the same value, exact); the second adds nothing
     relative(dx, slope, 1.6 * rel, ("slope", dtype))
+
+
+# With e = exp(-|x|), |x| <= 16: fp32's exponential (2 F), sum (F), quotient (F) and products (2 F) are off by 8 F
+# at most; 16-bit T's exponent, of at most 23.1, is rounded twice (2 * 23.1 ln 2 F = 32 F), its exponential,
+# reciprocal and products by 8 F more.
+SIGMOID_REL = {"f32": 8 * F, "f16": 40 * F, "bf16": 40 * F}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_sigmoid_slope_keeps_its_relative_accuracy(dtype):
+    """s (1 - s) of large x, where 1 - s is small."""
+    dt = T_OF[dtype]
+    x, eye = grid(-16.0, 16.0, dt), torch.eye(N, dtype=dt, device="cuda")
+    e = torch.exp(-x.double().abs())
+    exact = e / (1 + e) ** 2
+    dx, _, _ = hc.linear_backward(x, eye, torch.ones_like(x), x, activation="sigmoid")
+    relative(dx, exact, SIGMOID_REL[dtype], ("linear_backward", dtype))
+    zero, one = torch.zeros_like(eye), torch.ones_like(x)
+    dx = hc.glu_backward(x, eye, zero, x, one, one, activation="sigmoid")[0]  # u = dh = 1: dg Wg^T + du 0
+    relative(dx, exact, SIGMOID_REL[dtype], ("glu_backward", dtype))
+
+
+def test_slopes_of_large_preactivations_reach_one():
+    """The slopes of silu and gelu_tanh hold a factor 1 - s that x (and its cube) multiply."""
+    x, eye = grid(2.0, 12.0, torch.float32), torch.eye(N, device="cuda")
+    xd = x.double()
+    for act in ("silu", "gelu_tanh"):
+        dx, _, _ = hc.linear_backward(x, eye, torch.ones_like(x), x, activation=act)
+        if act == "silu":
+            e = torch.exp(-xd)
+            exact = (1 + xd * e / (1 + e)) / (1 + e)
+        else:  # with t the tanh form's argument: s = sigmoid(2 t)
+            c = (2 / math.pi) ** 0.5
+            e = torch.exp(-2 * c * (xd + 0.044715 * xd ** 3))
+            s = 1 / (1 + e)
+            exact = s + 2 * xd * s * (e * s) * c * (1 + 3 * 0.044715 * xd * xd)
+        # silu, s (1 + x c): x c <= 0.24 is off by 6 F of itself, the sum, s and the product by 5 F: 7 F in all.
+        # gelu_tanh, s + term: 2 t is rounded seven times, term <= 0.11 and term times 2 t <= 0.41, so the term is
+        # off by 7 * 0.41 F + 11 * 0.11 F, s by 3 F, the sum by F: 9 F in all.
+        relative(dx, exact, 9 * F, act)
