@@ -335,22 +335,27 @@ __device__ __forceinline__ u32x4 raw_desc(const void* base) {
 __device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(const lds_u8*)p; }
 // Lane l: W bytes (16 or 4) from offset off of the descriptor to LDS byte dst + W l (dst
 // the same in every lane). Written out because the compiler, which cannot tell the stage
-// being filled from the one being read, would wait for the load before every LDS read.
+// being filled from the one being read, would wait for the load before every LDS read. m0 is a
+// register of the compiler's own (it warns of any asm that writes it): named as written, so that
+// no value that the compiler put there itself is taken to have survived.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int W, bool STREAM> __device__ __forceinline__ void lds_load(u32x4 desc, uint32_t off, uint32_t dst) {
   static_assert(W == 16 || W == 4, "width");
   if constexpr (W == 4 && STREAM)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen nt lds"
-                 : : "s"(dst), "v"(off), "s"(desc) : "memory");
+                 : : "s"(dst), "v"(off), "s"(desc) : "memory", "m0");
   else if constexpr (W == 4)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 : : "s"(dst), "v"(off), "s"(desc) : "memory");
+                 : : "s"(dst), "v"(off), "s"(desc) : "memory", "m0");
   else if constexpr (STREAM)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
-                 : : "s"(dst), "v"(off), "s"(desc) : "memory");
+                 : : "s"(dst), "v"(off), "s"(desc) : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 : : "s"(dst), "v"(off), "s"(desc) : "memory");
+                 : : "s"(dst), "v"(off), "s"(desc) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Where an operand's next tile starts and how many contraction indices it has from
 // there in its segment; steps go through the first segment, then the second.
