@@ -18,6 +18,7 @@ ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigm
 NORM_MAX_HIDDEN = 32768
 MAX_ROWS = 1 << 21
 PRODUCT_MAX_WIDTH = 1 << 21
+COUNTER_BYTES = 4096
 
 EXPORTED = ("hclrmix_residual_norm", "hclrmix_residual_norm_workspace_size", "hclrmix_residual_norm_backward",
             "hclrmix_linear", "hclrmix_linear_backward", "hclrmix_glu", "hclrmix_glu_backward",
@@ -220,7 +221,9 @@ def _dense(t, like, shape, name):
 
 def _scratch(workspace, need, device):
     if workspace is None:
-        return torch.zeros(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace[:COUNTER_BYTES].zero_()  # the arrival counters; the rest may hold anything
+        return workspace
     if workspace.device != device or not workspace.is_contiguous():
         _refuse("workspace must be contiguous and on the tensors' device")
     return workspace
@@ -302,7 +305,7 @@ def residual_norm_backward(y, residual_out, d_residual_out=None, d_normed=None, 
     _dense(post_scale, y, shape[1:], "post_scale")
     _dense(pre_scale, y, shape[1:], "pre_scale")
     if workspace is None and (post_scale is not None or pre_scale is not None):
-        workspace = torch.zeros(hclrmix_residual_norm_workspace_size(p), dtype=torch.uint8, device=y.device)
+        workspace = _scratch(None, hclrmix_residual_norm_workspace_size(p), y.device)
     elif workspace is not None:
         _scratch(workspace, 0, y.device)
     dy, dr = torch.empty_like(y), torch.empty_like(y)
