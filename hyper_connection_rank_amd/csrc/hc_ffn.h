@@ -319,9 +319,7 @@ struct Product {
   int act;
 };
 
-// Bytes of split-sum scratch a product may use (without the counters).
-size_t product_scratch(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch);
-// scratch: product_scratch() bytes; counters: HCLRMIX_COUNTER_BYTES, zero.
+// scratch: product_scratch() bytes (hc_plan.h); counters: HCLRMIX_COUNTER_BYTES, zero.
 hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* counters, hipStream_t s);
 
 // dz = dy * act'(p) [rows, cols] into d0 and, with partial not null, the column sums of dz

@@ -8,6 +8,7 @@
 
 #include "hc_ffn.h"
 #include "hc_internal.h"
+#include "hc_plan.h"
 #include "hc_status.h"
 
 namespace {

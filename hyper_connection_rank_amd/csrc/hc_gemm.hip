@@ -22,16 +22,13 @@
 // epilogue.
 #include "hc_ffn.h"
 #include "hc_internal.h"
+#include "hc_plan.h"
 
 #include "../../include/hclrmix.h"
 
 #include <algorithm>
 
 namespace hc {
-
-// Most workgroup tiles of a product whose contraction is split: one arrival
-// counter each in the workspace's prefix.
-constexpr int MAX_SPLIT_TILES = HCLRMIX_COUNTER_BYTES / 4;
 
 // Kernel arguments: a Product and its schedule.
 struct Gemm {
@@ -755,124 +752,7 @@ __global__ __launch_bounds__(512) void k_product_wide(const Gemm a) {
   }
 }
 
-// ------------------------------------------------------------------ schedule
-
-constexpr int CUS = 256;
-
-// A tile shape, and the times (microseconds) of its model.
-struct Shape {
-  int bm, bn, bk, slots;  // slots: workgroups the chip runs at once, 1 to 3 per compute unit
-  double step, floor;     // one contraction step with every slot of a compute unit in use, and at least
-  double fixed;           // per tile: launch, first loads, epilogue
-  double join, rate;      // split tiles: per part read by the workgroup that joins it, and the rate
-                          // (TB/s) at which the parts are written and read
-};
-
-// Tile shape and split of a product.
-struct Plan {
-  const Shape* shape;
-  int tiles_m, tiles_n;
-  int64_t whole, rest;  // tiles taken whole, and split
-  int splits;           // parts of each split tile
-  double us;            // what the model expects
-};
-
-// A shape's tiles run in rounds of `slots` workgroups. Full rounds take their tiles whole; the
-// tiles left over (all of them, where there are fewer than slots) are split along the
-// contraction where that ends sooner: parts run shorter, but they are written and read again,
-// and the last one to arrive reads them all. The shapes' times were fitted to 8,500 measured
-// combinations of shape, split and product (1 to 8192 rows; ten weights from 2000 x 160 to
-// 10240 x 2560; all three operand layouts, aligned and not, bf16 and fp32): the model's error
-// has a standard deviation of about 12 %, and the plans it picks took 3 % more time on average
-// than the best ones measured (56 % at worst).
-static Plan shape_plan(const Shape& sh, int64_t M, int64_t N, int64_t K, bool dual, int segments, int batch) {
-  Plan p{};
-  p.shape = &sh;
-  const int cols = dual ? sh.bn / 2 : sh.bn;
-  p.tiles_m = (int)((M + sh.bm - 1) / sh.bm);
-  p.tiles_n = (int)((N + cols - 1) / cols);
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * batch;
-  const int64_t steps = (K + sh.bk - 1) / sh.bk * segments;
-  const int64_t rounds = tiles / sh.slots, rest = tiles % sh.slots;
-  auto time = [&](int64_t wgs, int64_t n) {  // of wgs workgroups of n steps
-    const double full = (double)(wgs / sh.slots) * (n * sh.step + sh.fixed);
-    const int64_t left = wgs % sh.slots;
-    const int64_t each = (left + CUS - 1) / CUS;  // of the compute units that have most
-    return full + (left ? n * std::max(sh.floor, sh.step * each * CUS / sh.slots) + sh.fixed : 0.0);
-  };
-  int splits = 1;
-  double best = time(rest, steps);
-  if (rest && rest <= MAX_SPLIT_TILES) {
-    for (int s = 2; s <= 64 && 2 * s <= steps && rest * s <= 2 * sh.slots; ++s) {
-      const double traffic = 8.0 * rest * s * std::min<int64_t>(sh.bm, M) * sh.bn;
-      const double t = time(rest * s, (steps + s - 1) / s) + (s + 3) * sh.join + traffic / (sh.rate * 1e6);
-      if (t < best) {
-        best = t;
-        splits = s;
-      }
-    }
-  }
-  p.splits = splits;
-  p.rest = splits > 1 ? rest : 0;
-  p.whole = tiles - p.rest;
-  p.us = time(rounds * sh.slots, steps) + best;
-  return p;
-}
-
-constexpr Shape WIDE{256, 256, 64, 256, 1.488, 0.071, 10.116, 1.738, 8.9};
-constexpr Shape MID{128, 128, 64, 512, 1.211, 0.787, 4.645, 0.607, 6.5};
-constexpr Shape F64{64, 64, 64, 768, 0.826, 0.347, 3.790, 0.422, 13.1};
-constexpr Shape F64D{64, 128, 64, 512, 1.164, 0.694, 1.541, 0.918, 9.6};
-constexpr Shape F64W{64, 256, 64, 256, 0.722, 0.735, 5.175, 0.544, 6.2};
-constexpr Shape F16{16, 64, 64, 768, 0.862, 0.400, 5.099, 0.083, 7.3};
-constexpr Shape F16D{16, 128, 64, 512, 1.310, 0.709, 1.857, 0.423, 3.1};
-constexpr Shape F16W{16, 256, 64, 256, 0.737, 0.626, 4.047, 0.419, 2.4};
-// 16-bit operands that are not 16-byte aligned, and fp32.
-constexpr Shape U128{128, 128, 64, 512, 1.682, 1.934, 4.764, 0.518, 5.0};
-constexpr Shape U64{64, 64, 64, 1024, 1.908, 0.857, 4.768, 0.302, 6.7};
-constexpr Shape U64D{64, 128, 64, 768, 2.191, 1.832, 2.396, 0.705, 6.7};
-constexpr Shape U16{16, 64, 64, 1024, 1.829, 0.744, 4.963, 0.118, 4.2};
-constexpr Shape U16D{16, 128, 64, 768, 2.700, 1.436, 2.938, 0.241, 20.0};
-constexpr Shape S128{128, 128, 32, 512, 4.129, 2.306, 5.816, 0.491, 6.3};
-constexpr Shape S64{64, 64, 32, 768, 1.859, 0.818, 4.282, 0.352, 9.4};
-constexpr Shape S64D{64, 128, 32, 512, 2.369, 1.428, 4.227, 0.696, 10.4};
-constexpr Shape S16{16, 64, 32, 768, 0.968, 0.378, 6.002, 0.093, 20.0};
-constexpr Shape S16D{16, 128, 32, 512, 1.163, 0.053, 5.300, 0.182, 20.0};
-
-static Plan make_plan(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch,
-                      bool aln) {
-  Plan best{};
-  auto consider = [&](const Shape& s) {
-    const Plan p = shape_plan(s, M, N, K, dual, segments, batch);
-    if (!best.shape || p.us < best.us) best = p;
-  };
-  const bool f32 = dtype == HCLRMIX_F32, few = M <= 16 && !p_trans;
-  if (f32 || !aln) {
-    consider(f32 ? S128 : U128);
-    consider(f32 ? (dual ? S64D : S64) : (dual ? U64D : U64));
-    if (few) consider(f32 ? (dual ? S16D : S16) : (dual ? U16D : U16));
-  } else {
-    consider(MID);
-    consider(WIDE);
-    consider(dual ? F64D : F64);
-    if (!p_trans) consider(F64W);
-    if (few) {
-      consider(dual ? F16D : F16);
-      consider(F16W);
-    }
-  }
-  return best;
-}
-
-size_t product_scratch(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch) {
-  if (M == 0 || K == 0) return 0;
-  size_t most = 0;
-  for (int aln = 0; aln < 2; ++aln) {
-    const Plan p = make_plan(dtype, M, N, K, p_trans, dual, segments, batch, aln != 0);
-    most = std::max(most, (size_t)p.rest * p.splits * p.shape->bm * p.shape->bn * 4);
-  }
-  return most;
-}
+// ------------------------------------------------------------------ launches
 
 // k_product_ring for one tile shape; rows staged through registers take two buffers.
 template <DT D, bool PT, bool QT, bool DUAL, int BM, int BN, int NST, int WM, int WN>
