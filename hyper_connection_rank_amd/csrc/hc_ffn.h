@@ -287,8 +287,9 @@ struct NormArgs {
 };
 
 hipError_t launch_norm(const NormArgs& a, int dtype, bool aligned, hipStream_t s);
-// Workgroups of the backward kernel, each with one row of partial sums.
-int norm_backward_groups(int64_t rows, int64_t hidden);
+// Workgroups of the backward kernel, each with one row of partial sums: at most this many for
+// this many rows or fewer.
+int norm_backward_most_groups(int64_t rows, int64_t hidden);
 hipError_t launch_norm_backward(const NormArgs& a, int dtype, bool aligned, hipStream_t s);
 
 // out0[c], out1[c] (each or null) = T(sum over r, in a fixed order, of partial[r * pitch + c]

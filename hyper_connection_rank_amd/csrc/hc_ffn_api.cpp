@@ -106,7 +106,7 @@ Range gate_span(const char* name, const void* gate, const hclrmix_norm_problem* 
 }
 
 size_t norm_workspace(const hclrmix_norm_problem* p) {
-  return HCLRMIX_COUNTER_BYTES + up256((size_t)hc::norm_backward_groups(p->rows, p->hidden) * 2 * (size_t)p->hidden * 4);
+  return HCLRMIX_COUNTER_BYTES + up256((size_t)hc::norm_backward_most_groups(p->rows, p->hidden) * 2 * (size_t)p->hidden * 4);
 }
 
 // ------------------------------------------------------------------ products

@@ -46,7 +46,7 @@ struct Gemm {
   int whole;        // tiles taken by one workgroup each (the first ones); the rest are split
   int splits;       // parts of a split tile
   int vec8;         // N is a multiple of 8 and every [M, N] tensor and bias 16-byte aligned
-  float* partial;   // [split tile][split][BM * BN] fp32
+  float* partial;   // [split tile][split][min(BM, M) * BN] fp32
   unsigned* counters;
 };
 
@@ -230,14 +230,15 @@ constexpr int AGENT = 16;  // sc1: the access is coherent across the chip's L2s
 // Split sums: this workgroup's tile goes to scratch; the last of the tile's workgroups to
 // arrive gets the sum of all parts in ascending order and true, the others false. A part is
 // [columns / 4][rows that exist] of four floats: vector i of a thread is row row(i) and
-// column group quad(i), and rows past the last one are neither written nor read.
+// column group quad(i), and rows past the last one are neither written nor read. A tile's parts
+// have room for part_size() floats each.
 template <int NA, int BM, int BN, typename Row, typename Quad>
 __device__ __forceinline__ bool join_splits(const Gemm& a, int slot, int split, int64_t m0, f32x4* acc, int tid, Row row,
                                             Quad quad) {
   __shared__ int is_last;
   const int rows = (int)min((int64_t)BM, a.M - m0);
   const uint32_t part = (uint32_t)rows * (BN / 4) * 16;  // bytes of one part
-  const char* base = (const char*)(a.partial + (size_t)slot * a.splits * (BM * BN));
+  const char* base = (const char*)(a.partial + (size_t)slot * a.splits * ((int)min((int64_t)BM, a.M) * BN));
   auto at = [&](int i) { return row(i) < rows ? (uint32_t)(quad(i) * rows + row(i)) * 16u : OUTSIDE; };
   {
     const rsrc_t r = make_rsrc(base + (size_t)split * part, part);

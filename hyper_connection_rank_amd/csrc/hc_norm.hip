@@ -491,10 +491,16 @@ hipError_t launch_norm(const NormArgs& a, int dtype, bool aligned, hipStream_t s
 
 // Up to 4 rows one workgroup takes them all and writes the scales' gradients itself: one
 // launch less. Above, every group adds 2 * hidden fp32 sums of traffic.
-int norm_backward_groups(int64_t rows, int64_t hidden) {
+static int64_t backward_most(const NormShape& sh) { return 256 * std::max(1, std::min(4, 16 / (sh.waves * sh.rows))); }
+static int norm_backward_groups(int64_t rows, int64_t hidden) {
   if (rows <= 4) return 1;
   const NormShape sh = norm_shape(hidden, true);
-  return norm_groups(rows, sh.rows, 256 * std::max(1, std::min(4, 16 / (sh.waves * sh.rows))));
+  return norm_groups(rows, sh.rows, backward_most(sh));
+}
+int norm_backward_most_groups(int64_t rows, int64_t hidden) {
+  if (rows <= 4) return 1;
+  const NormShape sh = norm_shape(hidden, true);
+  return (int)std::min((rows + sh.rows - 1) / sh.rows, backward_most(sh));
 }
 
 template <DT D, bool ALN, int NV, bool ONE, int WAVES, bool AHEAD>

@@ -97,40 +97,66 @@ constexpr Shape S64D{64, 128, 32, 512, 2.369, 1.428, 4.227, 0.696, 10.4};
 constexpr Shape S16{16, 64, 32, 768, 0.968, 0.378, 6.002, 0.093, 20.0};
 constexpr Shape S16D{16, 128, 32, 512, 1.163, 0.053, 5.300, 0.182, 20.0};
 
+// The shapes that a product may take: f(shape). few: for at most 16 rows only.
+template <typename F> inline void each_shape(int dtype, bool p_trans, bool dual, bool aln, F f) {
+  const bool f32 = dtype == HCLRMIX_F32, few = !p_trans;
+  if (f32 || !aln) {
+    f(f32 ? S128 : U128, false);
+    f(f32 ? (dual ? S64D : S64) : (dual ? U64D : U64), false);
+    if (few) f(f32 ? (dual ? S16D : S16) : (dual ? U16D : U16), true);
+  } else {
+    f(MID, false);
+    f(WIDE, false);
+    f(dual ? F64D : F64, false);
+    if (!p_trans) f(F64W, false);
+    if (few) {
+      f(dual ? F16D : F16, true);
+      f(F16W, true);
+    }
+  }
+}
+constexpr int64_t FEW_ROWS = 16;
+
 inline Plan make_plan(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch,
                       bool aln) {
   Plan best{};
-  auto consider = [&](const Shape& s) {
+  each_shape(dtype, p_trans, dual, aln, [&](const Shape& s, bool few) {
+    if (few && M > FEW_ROWS) return;
     const Plan p = shape_plan(s, M, N, K, dual, segments, batch);
     if (!best.shape || p.us < best.us) best = p;
-  };
-  const bool f32 = dtype == HCLRMIX_F32, few = M <= 16 && !p_trans;
-  if (f32 || !aln) {
-    consider(f32 ? S128 : U128);
-    consider(f32 ? (dual ? S64D : S64) : (dual ? U64D : U64));
-    if (few) consider(f32 ? (dual ? S16D : S16) : (dual ? U16D : U16));
-  } else {
-    consider(MID);
-    consider(WIDE);
-    consider(dual ? F64D : F64);
-    if (!p_trans) consider(F64W);
-    if (few) {
-      consider(dual ? F16D : F16);
-      consider(F16W);
-    }
-  }
+  });
   return best;
 }
 
-// Bytes of split-sum scratch a product may use (without the counters).
-inline size_t product_scratch(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments, int batch) {
+// Floats of one split tile's part: the rows that a tile can have.
+inline int64_t part_size(const Shape& sh, int64_t M) { return std::min<int64_t>(sh.bm, M) * sh.bn; }
+
+// Bytes of split-sum scratch (without the counters) that no plan of this product exceeds, nor of
+// one with fewer rows: rows are M, or K with p_trans. So it grows with the rows, though a plan's
+// own need does not, and a workspace for the most rows serves every call. With more rows a split
+// tile's parts never pass 2 * slots in all (fewer tiles or steps: what those allow).
+inline size_t product_scratch(int dtype, int64_t M, int64_t N, int64_t K, bool p_trans, bool dual, int segments,
+                              int batch) {
   if (M == 0 || K == 0) return 0;
-  size_t most = 0;
-  for (int aln = 0; aln < 2; ++aln) {
-    const Plan p = make_plan(dtype, M, N, K, p_trans, dual, segments, batch, aln != 0);
-    most = std::max(most, (size_t)p.rest * p.splits * p.shape->bm * p.shape->bn * 4);
-  }
-  return most;
+  int64_t most = 0;
+  for (int aln = 0; aln < 2; ++aln)
+    each_shape(dtype, p_trans, dual, aln != 0, [&](const Shape& s, bool few) {
+      const int64_t m = few ? std::min(M, FEW_ROWS) : M;
+      const int cols = dual ? s.bn / 2 : s.bn;
+      const int64_t tiles = (m + s.bm - 1) / s.bm * ((N + cols - 1) / cols) * batch;
+      const int64_t steps = (K + s.bk - 1) / s.bk * segments;
+      const int64_t splits = std::min<int64_t>(64, steps / 2);
+      if (splits < 2) return;
+      int64_t parts;
+      if (p_trans) {  // the same tiles for any number of rows
+        const int64_t rest = tiles % s.slots;
+        parts = rest ? rest * std::min(splits, 2 * s.slots / rest) : 0;
+      } else {
+        parts = std::min<int64_t>(2 * s.slots, std::min<int64_t>(tiles, s.slots - 1) * splits);
+      }
+      most = std::max(most, parts * part_size(s, m) * 4);
+    });
+  return (size_t)most;
 }
 
 }  // namespace hc

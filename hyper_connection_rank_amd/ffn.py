@@ -286,7 +286,7 @@ def residual_norm(y, residual=None, *, gate=None, post_scale=None, pre_scale=Non
 
 
 def residual_norm_workspace_size(rows: int, hidden: int, dtype) -> int:
-    """Bytes of the workspace of residual_norm_backward."""
+    """Bytes of the workspace of residual_norm_backward with up to that many rows."""
     return hclrmix_residual_norm_workspace_size(NormProblem(rows, hidden, 0, _CODES[dtype], 0, 0, 0, 1.0, 0.0))
 
 
@@ -340,13 +340,13 @@ def _weight(w, like, k, n, name) -> int:
 
 
 def linear_workspace_size(rows: int, width_in: int, width_out: int, dtype, *, backward=False) -> int:
-    """Bytes of the workspace of linear (or linear_backward) with any activation."""
+    """Bytes of the workspace of linear (or linear_backward) with any activation and up to that many rows."""
     p = Product(rows, width_in, width_out, 0, 0, 0, _CODES[dtype], ACTIVATIONS["silu"])
     return hclrmix_linear_backward_workspace_size(p) if backward else hclrmix_linear_workspace_size(p)
 
 
 def glu_workspace_size(rows: int, width_in: int, width_out: int, dtype, *, backward=False) -> int:
-    """Bytes of the workspace of glu (or glu_backward)."""
+    """Bytes of the workspace of glu (or glu_backward) with up to that many rows."""
     p = Product(rows, width_in, width_out, 0, 0, 0, _CODES[dtype], ACTIVATIONS["silu"])
     return hclrmix_glu_backward_workspace_size(p) if backward else hclrmix_glu_workspace_size(p)
 

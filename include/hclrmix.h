@@ -359,7 +359,7 @@ hclrmix_status hclrmix_residual_norm(const void* y, const void* residual, const 
                                      const hclrmix_norm_problem* problem, void* stream);
 
 /* Workspace of hclrmix_residual_norm_backward (partial sums of the two
- * scales' gradients). */
+ * scales' gradients): enough for this problem with rows or fewer rows. */
 hclrmix_status hclrmix_residual_norm_workspace_size(const hclrmix_norm_problem* problem, size_t* bytes);
 
 /* Gradients of hclrmix_residual_norm. Inputs: y, gate, post_scale, pre_scale
@@ -450,7 +450,9 @@ hclrmix_status hclrmix_glu_backward(const void* x, const void* gate_weight, cons
                                     const hclrmix_product* problem, void* stream);
 
 /* Workspace of each product call, for any choice of its optional tensors and
- * any strides. Every one is at least HCLRMIX_COUNTER_BYTES. */
+ * any strides, with rows or fewer rows: it grows with the rows, so one sized
+ * for the largest batch serves smaller ones. Every one is at least
+ * HCLRMIX_COUNTER_BYTES. */
 #define HCLRMIX_COUNTER_BYTES 4096
 hclrmix_status hclrmix_linear_workspace_size(const hclrmix_product* problem, size_t* bytes);
 hclrmix_status hclrmix_linear_backward_workspace_size(const hclrmix_product* problem, size_t* bytes);

@@ -12,12 +12,14 @@ from hyper_connection_rank_amd import build
 
 SOURCE = """
 #include "hc_plan.h"
-// [batch of queries][8]: dtype, M, N, K, p_trans, dual, segments, batch, aligned
+// [n][9]: dtype, M, N, K, p_trans, dual, segments, batch, aligned -> [n][8]: tile rows and columns, whole and split
+// tiles, parts of a split one, contraction step, scratch that is asked for, scratch that the plan uses
 extern "C" void plans(const long long* q, long long* r, long long n) {
-  for (long long i = 0; i < n; ++i, q += 9, r += 7) {
+  for (long long i = 0; i < n; ++i, q += 9, r += 8) {
     const hc::Plan p = hc::make_plan((int)q[0], q[1], q[2], q[3], q[4], q[5], (int)q[6], (int)q[7], q[8]);
     r[0] = p.shape->bm; r[1] = p.shape->bn; r[2] = p.whole; r[3] = p.rest; r[4] = p.splits; r[5] = p.shape->bk;
     r[6] = (long long)hc::product_scratch((int)q[0], q[1], q[2], q[3], q[4], q[5], (int)q[6], (int)q[7]);
+    r[7] = p.rest * p.splits * hc::part_size(*p.shape, q[1]) * 4;
   }
 }
 """
@@ -47,9 +49,9 @@ def products(rows, k, n, dtype):
 
 def ask(lib, queries):
     q = (ctypes.c_longlong * (9 * len(queries)))(*[v for t in queries for v in t])
-    r = (ctypes.c_longlong * (7 * len(queries)))()
+    r = (ctypes.c_longlong * (8 * len(queries)))()
     lib.plans(q, r, ctypes.c_longlong(len(queries)))
-    return [tuple(r[7 * i:7 * i + 7]) for i in range(len(queries))]
+    return [tuple(r[8 * i:8 * i + 8]) for i in range(len(queries))]
 
 
 def kind(plan):

@@ -2,6 +2,7 @@
 reaches the library."""
 from __future__ import annotations
 
+import pytest
 import torch
 
 import hyper_connection_rank_amd as hc
@@ -15,3 +16,17 @@ def test_a_workspace_of_the_call_s_own_has_only_its_counters_cleared(monkeypatch
     assert ws.numel() == 1 << 20 and ws.dtype == torch.uint8
     assert not ws[:4096].any()
     assert (ws[4096:] == 0xA5).all()
+
+
+ROWS = sorted(set(range(1, 80)) | {2 ** i + d for i in range(6, 14) for d in (-1, 0, 1)} | set(range(100, 4200, 300)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("k,n", [(2560, 10240), (10240, 2560), (2056, 136), (777, 4105)])
+def test_a_workspace_for_the_most_rows_serves_fewer(k, n, dtype):
+    for size in (hc.linear_workspace_size, hc.glu_workspace_size):
+        for backward in (False, True):
+            need = [size(r, k, n, dtype, backward=backward) for r in ROWS]
+            assert need == sorted(need), (size.__name__, backward)
+    need = [hc.residual_norm_workspace_size(r, k, dtype) for r in ROWS]
+    assert need == sorted(need)

@@ -1,6 +1,9 @@
 """The products' schedule on the CPU: the GPU tests' sizes take every plan that
-calls in the operators' range take."""
+calls in the operators' range take, and the scratch that is asked for holds the
+parts of every plan, of fewer rows too."""
 from __future__ import annotations
+
+import random
 
 import pytest
 
@@ -32,6 +35,20 @@ def test_every_plan_of_the_range_is_tested(lib):
 def test_split_tiles_of_the_second_weight(lib):
     """One launch of both weights' gradients whose split tiles lie in the second one's."""
     q = P.products(1229, 8264, 904, "bf16")["dw of glu"]
-    bm, bn, whole, rest, splits, _, _ = P.ask(lib, [q])[0]
+    bm, bn, whole, rest, splits = P.ask(lib, [q])[0][:5]
     tiles = -(-q[1] // bm) * -(-q[2] // bn)
     assert (bm, bn) == (256, 256) and splits > 1 and rest > 0 and whole >= tiles
+
+
+def test_scratch_holds_every_plan_of_as_many_rows_or_fewer(lib):
+    rng = random.Random(3)
+    # beside the operators' range, widths whose tiles leave any remainder, at every row count up to two tiles
+    calls = P.sample(8000, seed=5) + [(m, 2560, n, d) for m in range(1, 513) for n in (136, 2056, 10240) for d in ("bf16", "f32")]
+    large, small = [], []
+    for m, k, n, dtype in calls:
+        r = rng.randint(1, m)
+        for name, q in P.products(m, k, n, dtype).items():
+            large.append(q)
+            small.append(P.products(r, k, n, dtype)[name])
+    for q, a, b in zip(large, P.ask(lib, large), P.ask(lib, small)):
+        assert a[7] <= a[6] and b[7] <= b[6] <= a[6], (q, a, b)
