@@ -5,7 +5,8 @@ epilogue (linear), each with its gradients.
 Functions with the C names (``include/hclrmix.h``) marshal tensors and a
 problem struct; residual_norm(), linear(), glu() and their ``*_backward``
 take torch tensors alone, check them and allocate the outputs. A call is
-enqueued on the current stream of its tensors' device.
+enqueued on the current stream of its tensors' device. Autograd records none
+of them: while it records, tensors that require gradients are refused.
 """
 from __future__ import annotations
 
@@ -219,6 +220,15 @@ def _dense(t, like, shape, name):
         _refuse(f"{name} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _unrecorded(*tensors):
+    """Refuses tensors that require gradients while autograd records: the outputs would come back detached."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                _refuse("autograd does not record this call: make it under torch.no_grad() (or in a "
+                        "torch.autograd.Function) and take the gradients from the *_backward function")
+
+
 def _scratch(workspace, need, device):
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -270,6 +280,7 @@ def residual_norm(y, residual=None, *, gate=None, post_scale=None, pre_scale=Non
     (residual_out, normed). Returns them; normed is None with
     ``want_normed=False`` (pre_scale must then be None).
     """
+    _unrecorded(y, residual, gate, post_scale, pre_scale)
     p = _norm_problem(y, gate, post_norm, alpha, epsilon)
     shape = (p.rows, p.hidden)
     _dense(residual, y, shape, "residual")
@@ -298,6 +309,7 @@ def residual_norm_backward(y, residual_out, d_residual_out=None, d_normed=None, 
     that were not given. ``workspace``: a uint8 device buffer, zero-filled
     before its first use, of residual_norm_workspace_size bytes.
     """
+    _unrecorded(y, residual_out, d_residual_out, d_normed, gate, post_scale, pre_scale)
     p = _norm_problem(y, gate, post_norm, alpha, epsilon)
     shape = (p.rows, p.hidden)
     for t, name in ((residual_out, "residual_out"), (d_residual_out, "d_residual_out"), (d_normed, "d_normed")):
@@ -358,6 +370,7 @@ def linear(x, weight, bias=None, residual=None, *, activation="none", save=False
     linear_backward. ``out`` may supply y. ``workspace``: a uint8 device
     buffer, zero-filled before its first use, of linear_workspace_size bytes.
     """
+    _unrecorded(x, weight, bias, residual)
     code = _code(x, "x")
     rows, k = _rows_of(x, "x")
     n = weight.shape[-1]
@@ -379,6 +392,7 @@ def linear_backward(x, weight, dy, preact=None, *, activation="none", bias=False
     """Gradients of linear from dy [..., out] and, with an activation, the saved
     preact. Returns (dx, d_weight, d_bias); d_bias is None without ``bias``.
     The residual's gradient is dy."""
+    _unrecorded(x, weight, dy, preact)
     code = _code(x, "x")
     rows, k = _rows_of(x, "x")
     n = weight.shape[-1]
@@ -410,6 +424,7 @@ def glu(x, gate_weight, up_weight, gate_bias=None, up_bias=None, *, activation="
     [..., out]; with ``save`` (h, g, u) for glu_backward. ``workspace``: a
     uint8 device buffer, zero-filled before its first use, of
     glu_workspace_size bytes."""
+    _unrecorded(x, gate_weight, up_weight, gate_bias, up_bias)
     p = _glu_problem(x, gate_weight, up_weight, activation)
     rows, n = p.rows, p.out
     _dense(gate_bias, x, (n,), "gate_bias")
@@ -428,6 +443,7 @@ def glu_backward(x, gate_weight, up_weight, g, u, dh, *, activation="silu", bias
     """Gradients of glu from its saved g and u and dh [..., out]. Returns
     (dx, d_gate_weight, d_up_weight, d_gate_bias, d_up_bias); the last two are
     None without ``bias``."""
+    _unrecorded(x, gate_weight, up_weight, g, u, dh)
     p = _glu_problem(x, gate_weight, up_weight, activation)
     rows, k, n = p.rows, p.in_, p.out
     for t, name in ((g, "g"), (u, "u"), (dh, "dh")):

@@ -30,3 +30,34 @@ def test_a_workspace_for_the_most_rows_serves_fewer(k, n, dtype):
             assert need == sorted(need), (size.__name__, backward)
     need = [hc.residual_norm_workspace_size(r, k, dtype) for r in ROWS]
     assert need == sorted(need)
+
+
+def _calls():
+    """Every function's positional tensors and a call with them (CPU tensors: a call that is not refused before it
+    reaches the library is refused there, with another message)."""
+    t = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    y = lambda: t(4, 8)  # noqa: E731
+    return {"residual_norm": ([y(), y(), t(4), t(8), t(8)],
+                              lambda a, b, g, p, q: hc.residual_norm(a, b, gate=g, post_scale=p, pre_scale=q)),
+            "residual_norm_backward": ([y(), y(), y(), y(), t(4), t(8), t(8)],
+                                       lambda a, b, c, d, g, p, q: hc.residual_norm_backward(a, b, c, d, gate=g, post_scale=p,
+                                                                                             pre_scale=q)),
+            "linear": ([t(4, 8), t(8, 16), t(16), t(4, 16)], hc.linear),
+            "linear_backward": ([t(4, 8), t(8, 16), t(4, 16), t(4, 16)],
+                                lambda *a: hc.linear_backward(*a, activation="silu")),
+            "glu": ([t(4, 8), t(8, 16), t(8, 16), t(16), t(16)], hc.glu),
+            "glu_backward": ([t(4, 8), t(8, 16), t(8, 16), t(4, 16), t(4, 16), t(4, 16)], hc.glu_backward)}
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_tensors_that_require_gradients_are_refused_while_autograd_records(name):
+    tensors, call = _calls()[name]
+    for i, t in enumerate(tensors):
+        given = list(tensors)
+        given[i] = t.clone().requires_grad_()
+        with pytest.raises(hc.HclrmixError, match="autograd"):
+            call(*given)
+        with torch.no_grad(), pytest.raises(hc.HclrmixError, match="GPU"):
+            call(*given)
+    with pytest.raises(hc.HclrmixError, match="GPU"):
+        call(*tensors)
