@@ -51,15 +51,13 @@ template <DT D> __device__ __forceinline__ float phi_of(float x) {
   return D == DT::F32 ? 0.5f * erfcf(-x * RSQRT2) : phi_fast(x);
 }
 // s = sigmoid(x) and c = 1 - s, both with their full relative accuracy (a subtraction from one
-// would leave c, and so the slope s c, few correct bits for large x): with e = exp(-|x|) they are
-// 1 / (1 + e) and e / (1 + e).
+// would leave c, and so the slope s c, few correct bits for large x): with e = exp(-x) they are
+// 1 / (1 + e) and e / (1 + e). An infinite e is taken as the largest value, so that c stays finite
+// where s is 0.
 template <DT D> __device__ __forceinline__ void sigmoid_both(float x, float& s, float& c) {
-  const float a = fabsf(x);
-  const float e = D == DT::F32 ? expf(-a) : __builtin_amdgcn_exp2f(a * -1.4426950408889634f);
-  const float r = D == DT::F32 ? 1.0f / (1.0f + e) : __builtin_amdgcn_rcpf(1.0f + e);
-  const float q = e * r;
-  s = x < 0.0f ? q : r;
-  c = x < 0.0f ? r : q;
+  const float e = D == DT::F32 ? expf(-x) : __builtin_amdgcn_exp2f(x * -1.4426950408889634f);
+  s = D == DT::F32 ? 1.0f / (1.0f + e) : __builtin_amdgcn_rcpf(1.0f + e);
+  c = fminf(e, 3.4028234663852886e38f) * s;
 }
 __device__ __forceinline__ float relu(float x) { return x > 0.0f ? x : (x <= 0.0f ? 0.0f : x); }  // NaN stays NaN
 __device__ __forceinline__ float gelu_arg(float x) { return 2.0f * GELU_C * (x + GELU_A * x * x * x); }
