@@ -298,7 +298,7 @@ def residual_norm(y, residual=None, *, gate=None, post_scale=None, pre_scale=Non
 
 def residual_norm_workspace_size(rows: int, hidden: int, dtype) -> int:
     """Bytes of the workspace of residual_norm_backward with up to that many rows."""
-    return hclrmix_residual_norm_workspace_size(NormProblem(rows, hidden, 0, _CODES[dtype], 0, 0, 0, 1.0, 0.0))
+    return hclrmix_residual_norm_workspace_size(NormProblem(rows, hidden, 0, _dtype_code(dtype), 0, 0, 0, 1.0, 0.0))
 
 
 def residual_norm_backward(y, residual_out, d_residual_out=None, d_normed=None, *, gate=None, post_scale=None,
@@ -345,21 +345,33 @@ def _rows_of(t, name):
     return (t.numel() // cols if cols else 0), cols
 
 
-def _weight(w, like, k, n, name) -> int:
+def _columns(w, name) -> int:
     if w.dim() != 2:
-        _refuse(f"{name} must be [in, out]")
+        _refuse(f"{name} must be [in, out], got {tuple(w.shape)}")
+    return w.shape[1]
+
+
+def _weight(w, like, k, n, name) -> int:
+    _columns(w, name)
     return _matrix(w, like, k, n, name)
+
+
+def _dtype_code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        _refuse(f"unsupported dtype {dtype}", _UNSUPPORTED)
+    return code
 
 
 def linear_workspace_size(rows: int, width_in: int, width_out: int, dtype, *, backward=False) -> int:
     """Bytes of the workspace of linear (or linear_backward) with any activation and up to that many rows."""
-    p = Product(rows, width_in, width_out, 0, 0, 0, _CODES[dtype], ACTIVATIONS["silu"])
+    p = Product(rows, width_in, width_out, 0, 0, 0, _dtype_code(dtype), ACTIVATIONS["silu"])
     return hclrmix_linear_backward_workspace_size(p) if backward else hclrmix_linear_workspace_size(p)
 
 
 def glu_workspace_size(rows: int, width_in: int, width_out: int, dtype, *, backward=False) -> int:
     """Bytes of the workspace of glu (or glu_backward) with up to that many rows."""
-    p = Product(rows, width_in, width_out, 0, 0, 0, _CODES[dtype], ACTIVATIONS["silu"])
+    p = Product(rows, width_in, width_out, 0, 0, 0, _dtype_code(dtype), ACTIVATIONS["silu"])
     return hclrmix_glu_backward_workspace_size(p) if backward else hclrmix_glu_workspace_size(p)
 
 
@@ -373,7 +385,7 @@ def linear(x, weight, bias=None, residual=None, *, activation="none", save=False
     _unrecorded(x, weight, bias, residual)
     code = _code(x, "x")
     rows, k = _rows_of(x, "x")
-    n = weight.shape[-1]
+    n = _columns(weight, "weight")
     p = Product(rows, k, n, _matrix(x, x, rows, k, "x"), _weight(weight, x, k, n, "weight"), 0, code, _act(activation))
     _dense(bias, x, (n,), "bias")
     if residual is not None:
@@ -395,7 +407,7 @@ def linear_backward(x, weight, dy, preact=None, *, activation="none", bias=False
     _unrecorded(x, weight, dy, preact)
     code = _code(x, "x")
     rows, k = _rows_of(x, "x")
-    n = weight.shape[-1]
+    n = _columns(weight, "weight")
     p = Product(rows, k, n, _matrix(x, x, rows, k, "x"), _weight(weight, x, k, n, "weight"), 0, code, _act(activation))
     _dense(dy, x, (rows, n), "dy")
     _dense(preact, x, (rows, n), "preact")
@@ -409,7 +421,7 @@ def linear_backward(x, weight, dy, preact=None, *, activation="none", bias=False
 def _glu_problem(x, gate_weight, up_weight, activation):
     code = _code(x, "x")
     rows, k = _rows_of(x, "x")
-    n = gate_weight.shape[-1]
+    n = _columns(gate_weight, "gate_weight")
     stride = _weight(gate_weight, x, k, n, "gate_weight")
     if _weight(up_weight, x, k, n, "up_weight") != stride:
         _refuse("gate_weight and up_weight must have the same row stride")

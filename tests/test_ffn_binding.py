@@ -61,3 +61,28 @@ def test_tensors_that_require_gradients_are_refused_while_autograd_records(name)
             call(*given)
     with pytest.raises(hc.HclrmixError, match="GPU"):
         call(*tensors)
+
+
+def _refused(f, *args, part="", **kw):
+    with pytest.raises(hc.HclrmixError) as e:
+        f(*args, **kw)
+    assert part in str(e.value), str(e.value)
+
+
+@pytest.mark.parametrize("shape", [(), (8,), (2, 8, 16)])
+def test_weights_that_are_no_matrices_are_refused(shape):
+    t = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    x, g, w = t(4, 8), t(4, 16), torch.zeros(shape, dtype=torch.bfloat16)
+    _refused(hc.linear, x, w, part="weight must be [in, out]")
+    _refused(hc.linear_backward, x, w, g, part="weight must be [in, out]")
+    for gate, up, name in ((w, t(8, 16), "gate_weight"), (t(8, 16), w, "up_weight")):
+        _refused(hc.glu, x, gate, up, part=name + " must be [in, out]")
+        _refused(hc.glu_backward, x, gate, up, g, g, g, part=name + " must be [in, out]")
+
+
+@pytest.mark.parametrize("dtype", [torch.float64, torch.int8, None])
+def test_workspace_sizes_of_other_types_are_refused(dtype):
+    _refused(hc.residual_norm_workspace_size, 4, 64, dtype, part="dtype")
+    for size in (hc.linear_workspace_size, hc.glu_workspace_size):
+        for backward in (False, True):
+            _refused(size, 4, 64, 64, dtype, backward=backward, part="dtype")
