@@ -260,13 +260,17 @@ _PLAIN = {"norm": _plain_norm, "norm_back": _plain_norm_back, "glu": _plain_glu,
 
 # ---------------------------------------------------------------- the library's calls
 
-def _workspace(s, nbytes):
-    """The workspace that a program keeps for this state's calls, its arrival counters cleared before the first one.
-    Calls that may overlap (other streams, graphs) have states, and so workspaces, of their own."""
-    if "workspace" not in s:
-        s["workspace"] = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-        s["workspace"][:4096].zero_()
-    return s["workspace"]
+_kept = {}  # workspaces by device and stream, the largest last; none is freed, since a captured graph may use it
+
+
+def _workspace(nbytes):
+    """The zero-filled workspace that a program keeps for the calls on its stream, grown to the largest (outside a
+    capture, as its first calls are)."""
+    device = torch.cuda.current_device()
+    kept = _kept.setdefault((device, torch._C._cuda_getCurrentRawStream(device)), [])
+    if not kept or kept[-1].numel() < nbytes:
+        kept.append(torch.zeros(nbytes, dtype=torch.uint8, device="cuda"))
+    return kept[-1]
 
 
 def _own(s):
@@ -278,7 +282,7 @@ def _own(s):
                                 post_norm=c["post"], alpha=_ALPHA, epsilon=_EPS)
         return {"residual_out": r, "normed": n}
     if op == "norm_back":
-        ws = _workspace(s, hc.residual_norm_workspace_size(c["rows"], c["hidden"], s["y"].dtype))
+        ws = _workspace(hc.residual_norm_workspace_size(c["rows"], c["hidden"], s["y"].dtype))
         dy, dr, dg, dpost, dpre = hc.residual_norm_backward(
             s["y"], s["residual"], s["d_residual_out"], s["d_normed"], gate=s["gate"], post_scale=s["post_scale"],
             pre_scale=s["pre_scale"], post_norm=c["post"], alpha=_ALPHA, epsilon=_EPS, workspace=ws)
@@ -291,7 +295,7 @@ def _own(s):
         return out
     back = op.endswith("back")
     size = hc.glu_workspace_size if op.startswith("glu") else hc.linear_workspace_size
-    ws = _workspace(s, size(c["rows"], c["in"], c["out"], s["x"].dtype, backward=back))
+    ws = _workspace(size(c["rows"], c["in"], c["out"], s["x"].dtype, backward=back))
     if op == "glu":
         got = hc.glu(s["x"], s["wg"], s["wu"], s["bg"], s["bu"], activation=c["act"], save=c["save"], workspace=ws)
         return dict(zip(("h", "g", "u"), got)) if c["save"] else {"h": got}
