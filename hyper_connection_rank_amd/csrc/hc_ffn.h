@@ -325,6 +325,11 @@ hipError_t launch_product(const Product& p, int dtype, void* scratch, unsigned* 
 // before its rounding into b0 [cols] (partial: grad_groups(rows) rows of scratch). Glu form
 // (u not null): d0 = dy * u * act'(p), d1 = dy * act(p), sums into b0 and b1, scratch rows of
 // 2 * cols. d0 and d1 may be null (only sums wanted).
+// dz is rounded to T because it is an operand of the 16-bit matrix units in both products that
+// follow. That costs their results one rounding more: 2.3e-3 from the 64-bit definition in bf16
+// (2.9e-4 in fp16, relative 2-norm), where one rounding of the result alone is 1.7e-3 (2.1e-4);
+// from the products of the rounded dz they are those 1.7e-3 (2.1e-4). A second product with what
+// the rounding left off would take that away for twice the matrix work.
 int grad_groups(int64_t rows);
 hipError_t launch_act_grad(const void* dy, const void* p, const void* u, void* d0, void* d1, float* partial, void* b0,
                            void* b1, int64_t rows, int64_t cols, int act, int dtype, bool aligned, hipStream_t s);

@@ -22,7 +22,9 @@
 // memory pipeline; the scales are loaded once.
 // Measured: forward 8192 x 2560 bf16 30 us (5.6 TB/s; a copy reaches 6.1), 8192 x 4096 fp16 46
 // (5.8); backward 8192 x 4096 fp16 69 us and 5 for the scales' gradients (5.4), 8192 x 2560
-// bf16 61 (4.1), 1021 x 2057 fp32 22 and 6 (2.4: two rows per workgroup, their latencies).
+// bf16 61 (4.1), 1021 x 2057 fp32 22 and 6 (2.4). Rows that are not 16-byte aligned are read and
+// written under a condition per chunk, so that the compiler waits for everything in flight (see
+// RowChunks): 8192 x 2057 bf16 33 us forward (4.1) and 90 backward (2.2).
 #include "hc_ffn.h"
 #include "hc_internal.h"
 
@@ -449,8 +451,13 @@ __global__ __launch_bounds__(256) void k_zero(uint16_t* p, int64_t n) {
 
 // Waves that share a row: rows of up to 512 elements one each, four to a workgroup; above,
 // one chunk a thread up to eight waves, then two and four chunks. Backward keeps eight waves
-// up to 16384 elements: with sixteen a thread has 128 registers, and the sums of its columns
-// go to scratch (8192 columns: 161 us against 102).
+// up to 16384 elements: with sixteen a thread has 128 registers instead of 256 (8192 columns: 161
+// us against 102). Up to two chunks a thread the registers suffice. Four (backward above 8192
+// columns) need more than there are: 224 to 660 bytes a thread go to scratch with eight waves and
+// 764 to 1232 with sixteen (above 16384 columns). In bf16 3200 x 10240 takes 218 us (1.8 TB/s),
+// 2000 x 16384 193 (2.0) and 1000 x 32768 443 (0.9). Forward four chunks (above 16384 columns) spill
+// 80 to 216 bytes in fp32 and 24 to 48 with a gate per element (1000 x 32768: fp32 121 us, 4.3
+// TB/s; bf16 52, 5.1).
 struct NormShape {
   int nv, waves, threads, rows;  // rows per workgroup
 };
@@ -529,7 +536,7 @@ hipError_t launch_norm_backward(const NormArgs& a, int dtype, bool aligned, hipS
 
 hipError_t launch_column_sums(const float* partial, int nrows, int64_t pitch, int64_t cols, void* out0, void* out1,
                               int dtype, hipStream_t s) {
-  const bool vec = cols % 4 == 0 && pitch % 4 == 0;  // scratch itself is 256-byte aligned
+  const bool vec = cols % 4 == 0 && pitch % 4 == 0;  // scratch itself is 16-byte aligned
   const dim3 grid((unsigned)((cols + (vec ? 63 : 15)) / (vec ? 64 : 16)), out1 ? 2 : 1);
   auto run = [&](auto k4, auto k1) {
     return vec ? launch(nullptr, k4, grid, dim3(1024), 0, s, partial, nrows, pitch, cols, out0, out1)

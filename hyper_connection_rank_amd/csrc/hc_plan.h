@@ -38,11 +38,15 @@ struct Plan {
 // A shape's tiles run in rounds of `slots` workgroups. Full rounds take their tiles whole; the
 // tiles left over (all of them, where there are fewer than slots) are split along the
 // contraction where that ends sooner: parts run shorter, but they are written and read again,
-// and the last one to arrive reads them all. The shapes' times were fitted to 8,500 measured
-// combinations of shape, split and product (1 to 8192 rows; ten weights from 2000 x 160 to
-// 10240 x 2560; all three operand layouts, aligned and not, bf16 and fp32): the model's error
-// has a standard deviation of about 12 %, and the plans it picks took 3 % more time on average
-// than the best ones measured (56 % at worst).
+// and the last one to arrive reads them all.
+// The shapes' times were fitted to 8,500 measured combinations of shape, split and product (1 to
+// 8192 rows; ten weights from 2000 x 160 to 10240 x 2560; all three operand layouts, aligned and
+// not, bf16 and fp32). At the fit the model's error had a standard deviation of about 12 %, and
+// the plans it picked took 3 % more time on average than the best ones measured (56 % at worst).
+// The kernels have changed since, and the fit has not been repeated: the epilogue goes through
+// LDS by whole rows; unaligned fp32 operands are loaded 4 bytes at a time, straight into LDS, and
+// are planned with the times of aligned ones; F16's floor was set by hand (fitted: 0.175). How
+// far the model is from the present kernels is not known.
 inline Plan shape_plan(const Shape& sh, int64_t M, int64_t N, int64_t K, bool dual, int segments, int batch) {
   Plan p{};
   p.shape = &sh;
@@ -85,7 +89,7 @@ constexpr Shape F64W{64, 256, 64, 256, 0.722, 0.735, 5.175, 0.544, 6.2};
 constexpr Shape F16{16, 64, 64, 768, 0.862, 0.400, 5.099, 0.083, 7.3};
 constexpr Shape F16D{16, 128, 64, 512, 1.310, 0.709, 1.857, 0.423, 3.1};
 constexpr Shape F16W{16, 256, 64, 256, 0.737, 0.626, 4.047, 0.419, 2.4};
-// 16-bit operands that are not 16-byte aligned, and fp32.
+// U: 16-bit operands that are not 16-byte aligned; S: fp32, aligned or not.
 constexpr Shape U128{128, 128, 64, 512, 1.682, 1.934, 4.764, 0.518, 5.0};
 constexpr Shape U64{64, 64, 64, 1024, 1.908, 0.857, 4.768, 0.302, 6.7};
 constexpr Shape U64D{64, 128, 64, 768, 2.191, 1.832, 2.396, 0.705, 6.7};

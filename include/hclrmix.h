@@ -419,8 +419,10 @@ hclrmix_status hclrmix_linear(const void* x, const void* weight, const void* bia
  * d_weight = x^T @ dz [in, out], d_bias = sums of dz over the rows [out];
  * each NULL when not wanted, at least one wanted (weight may be NULL without
  * dx, x without d_weight). residual's gradient is dy itself. The two
- * products take dz rounded to T, d_bias takes it before that rounding. With
- * rows == 0, d_weight and d_bias are zeros. */
+ * products take dz rounded to T, as the matrix units' 16-bit operands (so dx
+ * and d_weight are off by two roundings instead of one, and an fp16 dz has
+ * fp16's range); d_bias takes it before that rounding. With rows == 0,
+ * d_weight and d_bias are zeros. */
 hclrmix_status hclrmix_linear_backward(const void* x, const void* weight, const void* preact, const void* dy, void* dx,
                                        void* d_weight, void* d_bias, void* workspace, size_t workspace_bytes,
                                        const hclrmix_product* problem, void* stream);
@@ -442,7 +444,8 @@ hclrmix_status hclrmix_glu(const void* x, const void* gate_weight, const void* u
  * Each output may be NULL when not wanted, but the two weights' gradients
  * only together, and the two biases' likewise; at least one wanted (the
  * weights may be NULL without dx, x without the weights' gradients). The
- * products take dg and du rounded to T, the bias sums before that rounding.
+ * products take dg and du rounded to T (see hclrmix_linear_backward), the
+ * bias sums before that rounding.
  * With rows == 0, the weights' and biases' gradients are zeros. */
 hclrmix_status hclrmix_glu_backward(const void* x, const void* gate_weight, const void* up_weight, const void* g,
                                     const void* u, const void* dh, void* dx, void* d_gate_weight, void* d_up_weight,
