@@ -101,6 +101,7 @@ def library(path: Optional[str] = None):
     lib.hclrmix_version.restype = ctypes.c_char_p
     lib.hclrmix_version.argtypes = []
     ffn.declare(lib)
+    attn.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -332,4 +333,12 @@ from .ffn import (  # noqa: E402
     hclrmix_residual_norm_workspace_size, linear, linear_backward, linear_workspace_size, residual_norm,
     residual_norm_backward, residual_norm_workspace_size)
 
-EXPORTED = EXPORTED + ffn.EXPORTED
+from . import attn  # noqa: E402
+from .attn import (  # noqa: E402
+    ATTENTION_MAX_BATCH, ATTENTION_MAX_DIM, ATTENTION_MAX_HEADS, MAX_PAGE_SIZE, AttentionProblem, MapProblem, PagedProblem,
+    StoreProblem, attention, attention_backward, attention_workspace_size, cache_store, hclrmix_attention,
+    hclrmix_attention_backward, hclrmix_attention_backward_workspace_size, hclrmix_attention_workspace_size,
+    hclrmix_cache_store, hclrmix_page_map, hclrmix_paged_attention, hclrmix_paged_attention_workspace_size, page_map,
+    paged_attention, paged_attention_workspace_size)
+
+EXPORTED = EXPORTED + ffn.EXPORTED + attn.EXPORTED

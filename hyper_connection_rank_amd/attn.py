@@ -1,0 +1,384 @@
+"""Binding of the attention operators: attention over whole sequences with its
+gradients, one new token's attention over a cache in pages
+(paged_attention), rows stored into that cache (cache_store) and the tables
+that say where tokens live (page_map).
+
+Functions with the C names (``include/hclrmix.h``) marshal tensors and a
+problem struct; attention(), paged_attention(), cache_store(), page_map() and
+attention_backward() take torch tensors alone, check them and allocate the
+outputs. A call is enqueued on the current stream of its tensors' device.
+Autograd records none of them: while it records, tensors that require
+gradients are refused.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .ffn import _call, _code, _dtype_code, _p, _refuse, _same, _scratch, _size, _unrecorded, _ws
+
+ATTENTION_MAX_HEADS = 1024
+ATTENTION_MAX_DIM = 256
+ATTENTION_MAX_BATCH = 65536
+MAX_PAGE_SIZE = 65536
+
+EXPORTED = ("hclrmix_attention", "hclrmix_attention_backward", "hclrmix_attention_workspace_size",
+            "hclrmix_attention_backward_workspace_size", "hclrmix_paged_attention",
+            "hclrmix_paged_attention_workspace_size", "hclrmix_cache_store", "hclrmix_page_map")
+
+_I64, _I32, _F32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+def _strides(*names):
+    """The three fields of each hclrmix_strides member (sequence, token, head), laid out flat."""
+    return [(f"{n}_{d}", _I64) for n in names for d in ("sequence", "token", "head")]
+
+
+class AttentionProblem(ctypes.Structure):
+    _fields_ = [("batch", _I64), ("q_tokens", _I64), ("k_tokens", _I64), ("heads", _I32), ("kv_heads", _I32), ("dim", _I32),
+                ("dtype", _I32), ("causal", _I32), ("window", _I32), ("sinks", _I32), ("packed", _I32), ("scale", _F32),
+                ("reserved", _I32 * 2)] + _strides("q", "k", "v", "out", "d_out", "dq", "dk", "dv")
+
+
+class PagedProblem(ctypes.Structure):
+    _fields_ = [("batch", _I64), ("pages", _I64), ("page_size", _I64), ("most_pages", _I64), ("table_stride", _I64),
+                ("heads", _I32), ("kv_heads", _I32), ("dim", _I32), ("dtype", _I32), ("window", _I32), ("sinks", _I32),
+                ("scale", _F32), ("reserved", _I32)] + _strides("q", "out", "cache")
+
+
+class StoreProblem(ctypes.Structure):
+    _fields_ = [("tokens", _I64), ("pages", _I64), ("page_size", _I64), ("kv_heads", _I32), ("dim", _I32), ("dtype", _I32),
+                ("reserved", _I32)] + _strides("k", "v", "cache")
+
+
+class MapProblem(ctypes.Structure):
+    _fields_ = [("batch", _I64), ("tokens", _I64), ("page_size", _I64), ("most_pages", _I64), ("table_stride", _I64),
+                ("free_count", _I64), ("reserved", _I32)]
+
+
+def declare(lib) -> None:
+    """Argument types of this module's entry points."""
+    P, N = ctypes.c_void_p, ctypes.c_size_t
+    sig = {"hclrmix_attention": [P] * 8 + [N, P, P],
+           "hclrmix_attention_backward": [P] * 12 + [N, P, P],
+           "hclrmix_paged_attention": [P] * 7 + [N, P, P],
+           "hclrmix_cache_store": [P] * 7,
+           "hclrmix_page_map": [P] * 12}
+    for name in EXPORTED:
+        f = getattr(lib, name)
+        f.restype = ctypes.c_int
+        f.argtypes = sig.get(name, [P, P])
+
+
+# ---------------------------------------------------------------- the C names
+
+def hclrmix_attention(q, k, v, q_starts, k_starts, out, lse, workspace, problem: AttentionProblem) -> None:
+    _call("hclrmix_attention", q.device, _p(q), _p(k), _p(v), _p(q_starts), _p(k_starts), _p(out), _p(lse), *_ws(workspace),
+          ctypes.byref(problem))
+
+
+def hclrmix_attention_backward(q, k, v, out, lse, d_out, q_starts, k_starts, dq, dk, dv, workspace,
+                               problem: AttentionProblem) -> None:
+    _call("hclrmix_attention_backward", q.device, _p(q), _p(k), _p(v), _p(out), _p(lse), _p(d_out), _p(q_starts), _p(k_starts),
+          _p(dq), _p(dk), _p(dv), *_ws(workspace), ctypes.byref(problem))
+
+
+def hclrmix_attention_workspace_size(problem: AttentionProblem) -> int:
+    return _size("hclrmix_attention_workspace_size", problem)
+
+
+def hclrmix_attention_backward_workspace_size(problem: AttentionProblem) -> int:
+    return _size("hclrmix_attention_backward_workspace_size", problem)
+
+
+def hclrmix_paged_attention(q, k_cache, v_cache, table, lengths, out, workspace, problem: PagedProblem) -> None:
+    _call("hclrmix_paged_attention", q.device, _p(q), _p(k_cache), _p(v_cache), _p(table), _p(lengths), _p(out),
+          *_ws(workspace), ctypes.byref(problem))
+
+
+def hclrmix_paged_attention_workspace_size(problem: PagedProblem) -> int:
+    return _size("hclrmix_paged_attention_workspace_size", problem)
+
+
+def hclrmix_cache_store(k, v, slots, k_cache, v_cache, problem: StoreProblem) -> None:
+    _call("hclrmix_cache_store", k.device, _p(k), _p(v), _p(slots), _p(k_cache), _p(v_cache), ctypes.byref(problem))
+
+
+def hclrmix_page_map(cached, fresh, free_pages, free_start, table, starts, lengths, positions, slots, taken,
+                     problem: MapProblem) -> None:
+    _call("hclrmix_page_map", cached.device, _p(cached), _p(fresh), _p(free_pages), _p(free_start), _p(table), _p(starts),
+          _p(lengths), _p(positions), _p(slots), _p(taken), ctypes.byref(problem))
+
+
+# ---------------------------------------------------------------- tensors in, tensors out
+
+def _rows(t, like, shape, name):
+    """Checks t against a shape (its last dimension contiguous, no dimension expand()ed); returns (sequence, token, head)
+    strides, 0 for dimensions of one element or that it does not have."""
+    if t is not like:
+        _same(t, like, name)
+    if t.shape != shape:
+        _refuse(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        _refuse(f"{name}'s last dimension must be contiguous")
+    out = []
+    for n, s in zip(shape[:-1], st):
+        if n > 1 and s == 0:
+            _refuse(f"{name} must have rows of its own; expand()ed tensors are refused")
+        out.append(s if n > 1 else 0)
+    return (0,) * (3 - len(out)) + tuple(out)
+
+
+def _ints(t, like, shape, name):
+    """Checks a contiguous int32 tensor."""
+    if t.dtype is not torch.int32 or t.device != like.device:
+        _refuse(f"{name} must be an int32 tensor on the tensors' device")
+    if t.shape != shape or not t.is_contiguous():
+        _refuse(f"{name} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _scale_of(scale, dim):
+    return float(dim) ** -0.5 if scale is None else float(scale)
+
+
+def _count(x, name):
+    """A window or a count of first tokens."""
+    x = int(x)
+    if not 0 <= x < 1 << 31:
+        _refuse(f"{name} must be 0 to 2^31 - 1")
+    return x
+
+
+def _whole(q, k, v, causal, window, sinks, scale, q_starts, k_starts):
+    """(problem fields, strides of q, k, v) of attention over whole sequences."""
+    code = _code(q, "q")
+    if q.dim() not in (3, 4):
+        _refuse("q must be [batch, tokens, heads, dim], or [tokens, heads, dim]")
+    if k.dim() != q.dim():
+        _refuse("k must have as many dimensions as q")
+    packed = q_starts is not None
+    if packed and q.dim() != 3:
+        _refuse("packed sequences are [tokens, heads, dim]")
+    if k_starts is not None and not packed:
+        _refuse("k_starts without q_starts")
+    heads, dim = q.shape[-2:]
+    kv_heads, k_tokens = k.shape[-2], k.shape[-3]
+    batch = q.shape[0] if q.dim() == 4 else 1
+    shape = q.shape[:-3] + (k_tokens, kv_heads, dim)
+    if packed:
+        if q_starts.dim() != 1 or q_starts.shape[0] < 1:
+            _refuse("q_starts must be [sequences + 1]")
+        batch = q_starts.shape[0] - 1
+        _ints(q_starts, q, (batch + 1,), "q_starts")
+        if k_starts is not None:
+            _ints(k_starts, q, (batch + 1,), "k_starts")
+        elif k_tokens != q.shape[0]:
+            _refuse("k_starts may be left out only where q and k have the same rows")
+    st = _rows(q, q, q.shape, "q") + _rows(k, q, shape, "k") + _rows(v, q, shape, "v")
+    return (batch, q.shape[-3], k_tokens, heads, kv_heads, dim, code, 1 if causal else 0, _count(window, "window"),
+            _count(sinks, "sinks"), 1 if packed else 0, _scale_of(scale, dim), (_I32 * 2)()), st
+
+
+def attention(q, k, v, *, causal=True, window=0, sinks=0, scale=None, q_starts=None, k_starts=None, save=False, out=None,
+              workspace=None):
+    """Attention over whole sequences: out = softmax(scale q k^T) v over the keys that each query sees.
+
+    q [batch, q_tokens, heads, dim], k and v [batch, k_tokens, kv_heads, dim],
+    or without the batch, one sequence; any strides with a contiguous last
+    dimension (columns of a merged projection, heads before tokens). heads is
+    a multiple of kv_heads. With ``q_starts`` (int32 [sequences + 1], on the
+    device) the rows of q [tokens, heads, dim] are packed sequences,
+    ``k_starts`` likewise for k and v where they differ. Query i of a
+    sequence stands at p = i + k_len - q_len and sees keys j <= p
+    (``causal``), with a ``window`` those with |p - j| < window and the
+    first ``sinks`` keys. A query that sees no key gives zeros.
+
+    ``scale`` is dim ** -0.5 by default. ``out`` may supply the result.
+    Returns out, with ``save`` (out, lse), the fp32 [.., q_tokens, heads]
+    logarithms that attention_backward takes. Rows of packed tensors that
+    belong to no sequence are left as they were in a given ``out``, and are
+    zeros in tensors that the call allocates.
+    """
+    _unrecorded(q, k, v)
+    fields, st = _whole(q, k, v, causal, window, sinks, scale, q_starts, k_starts)
+    new = torch.empty if q_starts is None else torch.zeros
+    if out is None:
+        out = new(q.shape, dtype=q.dtype, device=q.device)
+    lse = new(q.shape[:-1], dtype=torch.float32, device=q.device) if save else None
+    p = AttentionProblem(*fields, *st, *_rows(out, q, q.shape, "out"))
+    if workspace is None:
+        need = hclrmix_attention_workspace_size(p)
+        workspace = _scratch(None, need, q.device)
+    else:
+        _scratch(workspace, 0, q.device)
+    hclrmix_attention(q, k, v, q_starts, k_starts, out, lse, workspace, p)
+    return (out, lse) if save else out
+
+
+def attention_backward(q, k, v, out, lse, d_out, *, causal=True, window=0, sinks=0, scale=None, q_starts=None, k_starts=None,
+                       grads=None, workspace=None):
+    """Gradients (dq, dk, dv) of attention from its inputs, the out and lse that it returned (``save``) and d_out.
+    ``grads`` may supply (dq, dk, dv), each None when not wanted: tensors of any strides, also columns of one merged
+    gradient; rows that belong to no sequence are left as they were there, and are zeros in tensors that the call
+    allocates."""
+    _unrecorded(q, k, v, out, d_out)
+    fields, st = _whole(q, k, v, causal, window, sinks, scale, q_starts, k_starts)
+    if lse.dtype is not torch.float32 or lse.device != q.device or lse.shape != q.shape[:-1] or not lse.is_contiguous():
+        _refuse(f"lse must be contiguous float32 {tuple(q.shape[:-1])}")
+    st += _rows(out, q, q.shape, "out") + _rows(d_out, q, q.shape, "d_out")
+    if grads is None:
+        new = torch.empty if q_starts is None else torch.zeros
+        grads = [new(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v)]
+    dq, dk, dv = grads
+    for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
+        st += (0, 0, 0) if t is None else _rows(t, q, like.shape, name)
+    p = AttentionProblem(*fields, *st)
+    if workspace is None:
+        need = hclrmix_attention_backward_workspace_size(p)
+        workspace = _scratch(None, need, q.device)
+    else:
+        _scratch(workspace, 0, q.device)
+    hclrmix_attention_backward(q, k, v, out, lse, d_out, q_starts, k_starts, dq, dk, dv, workspace, p)
+    return dq, dk, dv
+
+
+def attention_workspace_size(batch: int, q_tokens: int, k_tokens: int, heads: int, kv_heads: int, dim: int, dtype, *,
+                             packed=False, backward=False) -> int:
+    """Bytes of the workspace of attention (or attention_backward) with up to that many sequences and tokens (of each
+    sequence; packed: of all)."""
+    p = AttentionProblem(batch, q_tokens, k_tokens, heads, kv_heads, dim, _dtype_code(dtype), 0, 0, 0, 1 if packed else 0, 1.0)
+    return (hclrmix_attention_backward_workspace_size if backward else hclrmix_attention_workspace_size)(p)
+
+
+def _cache(k_cache, v_cache, like, kv_heads, dim):
+    """(pages, page_size) and the strides of both caches."""
+    if k_cache.dim() != 4 or k_cache.shape[2:] != (kv_heads, dim):
+        _refuse(f"k_cache must be [pages, page_size, {kv_heads}, {dim}], got {tuple(k_cache.shape)}")
+    st = _rows(k_cache, like, k_cache.shape, "k_cache")
+    if _rows(v_cache, like, k_cache.shape, "v_cache") != st:
+        _refuse("k_cache and v_cache must have the same strides")
+    return k_cache.shape[0], k_cache.shape[1], st
+
+
+def _table(table, like, batch, name="block_table"):
+    """(entries of a row, stride of a row) of a block table."""
+    if table.dtype is not torch.int32 or table.device != like.device:
+        _refuse(f"{name} must be an int32 tensor on the tensors' device")
+    if table.dim() != 2 or table.shape[0] != batch:
+        _refuse(f"{name} must be [{batch}, pages of a sequence], got {tuple(table.shape)}")
+    n, (row, col) = table.shape[1], table.stride()
+    if (col != 1 and n > 1) or (batch > 1 and row < n):
+        _refuse(f"{name}'s rows must be contiguous and its own")
+    return n, row if batch > 1 else 0
+
+
+def paged_attention(q, k_cache, v_cache, block_table, lengths, *, window=0, sinks=0, scale=None, out=None, workspace=None):
+    """Attention of one new token of each sequence over a key-value cache in pages.
+
+    q [sequences, heads, dim]; the caches [pages, page_size, kv_heads, dim],
+    of any strides, the same for both, with a contiguous last dimension;
+    block_table int32 [sequences, pages of a sequence]; lengths int32
+    [sequences], the new token (whose key and value are in the cache
+    already) counted. The token sees every key, with a ``window`` the last
+    ``window`` ones (its own among them) and the first ``sinks`` keys.
+    Entries of the table behind the last page, and those of pages outside
+    the window, may hold anything; keys on pages that the cache does not have
+    are not seen. A length of 0 gives zeros.
+    ``workspace``: a uint8 device buffer, zero-filled before its first use, of
+    paged_attention_workspace_size bytes.
+    """
+    _unrecorded(q, k_cache, v_cache)
+    code = _code(q, "q")
+    if q.dim() != 3:
+        _refuse("q must be [sequences, heads, dim]")
+    batch, heads, dim = q.shape
+    if k_cache.dim() != 4:
+        _refuse("k_cache must be [pages, page_size, kv_heads, dim]")
+    kv_heads = k_cache.shape[2]
+    pages, page_size, cache = _cache(k_cache, v_cache, q, kv_heads, dim)
+    most, stride = _table(block_table, q, batch)
+    _ints(lengths, q, (batch,), "lengths")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    sq, so = _rows(q, q, q.shape, "q"), _rows(out, q, q.shape, "out")
+    p = PagedProblem(batch, pages, page_size, most, stride, heads, kv_heads, dim, code, _count(window, "window"),
+                     _count(sinks, "sinks"), _scale_of(scale, dim), 0, sq[1], 0, sq[2], so[1], 0, so[2], *cache)
+    if workspace is None:
+        need = hclrmix_paged_attention_workspace_size(p)
+        workspace = _scratch(None, need, q.device)
+    else:
+        _scratch(workspace, 0, q.device)
+    hclrmix_paged_attention(q, k_cache, v_cache, block_table, lengths, out, workspace, p)
+    return out
+
+
+def paged_attention_workspace_size(batch: int, most_pages: int, page_size: int, heads: int, kv_heads: int, dim: int, dtype) -> int:
+    """Bytes of the workspace of paged_attention with up to that many sequences and pages of each."""
+    return hclrmix_paged_attention_workspace_size(
+        PagedProblem(batch, 0, page_size, most_pages, 0, heads, kv_heads, dim, _dtype_code(dtype), 0, 0, 1.0, 0))
+
+
+def cache_store(k, v, k_cache, v_cache, slots) -> None:
+    """Stores rows k and v [tokens, kv_heads, dim] into the caches [pages, page_size, kv_heads, dim] in place: row t goes
+    to row slots[t] % page_size of page slots[t] // page_size; rows whose slot (int32) is negative or outside the
+    cache go nowhere. A slot should occur once: of rows with the same slot, it is left open which one each element
+    is from."""
+    _unrecorded(k, v, k_cache, v_cache)
+    code = _code(k, "k")
+    if k.dim() != 3:
+        _refuse("k must be [tokens, kv_heads, dim]")
+    tokens, kv_heads, dim = k.shape
+    pages, page_size, cache = _cache(k_cache, v_cache, k, kv_heads, dim)
+    _ints(slots, k, (tokens,), "slots")
+    p = StoreProblem(tokens, pages, page_size, kv_heads, dim, code, 0, *_rows(k, k, k.shape, "k"), *_rows(v, k, k.shape, "v"), *cache)
+    hclrmix_cache_store(k, v, slots, k_cache, v_cache, p)
+
+
+def page_map(cached, fresh, block_table, free_pages, *, page_size: int, tokens: int, free_start=None, out=None):
+    """The tables of a step that brings fresh[b] new tokens to request b, which has cached[b] in the cache.
+
+    All tensors are int32 on the device: cached and fresh [requests],
+    block_table [requests, pages of a request], whose entries of new pages
+    are written in place, free_pages [count]: the pages that may be taken, in
+    order, from entry ``free_start`` ([1], default 0) on. ``tokens`` is the
+    number of rows of the step's batch, padding included.
+
+    Returns (starts [requests + 1], lengths [requests], positions [tokens],
+    slots [tokens], taken [requests + 1]): the packed sequences' starts for
+    attention, the lengths for paged_attention, each row's position in its
+    sequence and place in the cache for cache_store (0 and -1 for rows behind
+    the last request; -1 also where the pages have run out), and the sums of
+    the pages taken, the last of which moves free_start on. ``out`` may
+    supply the five. Repeating the call repeats its results.
+    """
+    if cached.dtype is not torch.int32 or cached.dim() != 1 or not cached.is_contiguous():
+        _refuse("cached must be a contiguous int32 tensor [requests]")
+    batch = cached.shape[0]
+    _ints(fresh, cached, (batch,), "fresh")
+    most, stride = _table(block_table, cached, batch)
+    if free_pages.dim() != 1:
+        _refuse("free_pages must be [count]")
+    _ints(free_pages, cached, free_pages.shape, "free_pages")
+    if free_start is not None:
+        _ints(free_start, cached, (1,), "free_start")
+    tokens, page_size = int(tokens), int(page_size)
+    if tokens < 0:
+        _refuse("tokens must be >= 0")
+    sizes = (batch + 1, batch, tokens, tokens, batch + 1)
+    if out is None:
+        # one allocation, each part on 16 bytes
+        first, parts = 0, []
+        for n in sizes:
+            parts.append(first)
+            first += (n + 3) & ~3
+        whole = torch.empty(first, dtype=torch.int32, device=cached.device)
+        out = [whole[i:i + n] for i, n in zip(parts, sizes)]
+    else:
+        for t, n, name in zip(out, sizes, ("starts", "lengths", "positions", "slots", "taken")):
+            _ints(t, cached, (n,), name)
+    starts, lengths, positions, slots, taken = out
+    p = MapProblem(batch, tokens, page_size, most, stride, free_pages.shape[0], 0)
+    hclrmix_page_map(cached, fresh, free_pages, free_start, block_table, starts, lengths, positions, slots, taken, p)
+    return starts, lengths, positions, slots, taken

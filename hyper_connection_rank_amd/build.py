@@ -18,8 +18,10 @@ PEAKS_LIB = os.path.join(HERE, "libhcpeaks.so")
 PEAKS_SOURCES = ["hc_peaks.hip"]
 
 SOURCES = ["hc_api.cpp", "hc_generic.hip", "hc_decode.hip", "hc_prefill.hip", "hc_invrms.hip", "hc_pad.hip",
-           "hc_ffn_api.cpp", "hc_norm.hip", "hc_gemm.hip"]
-HEADERS = ["hc_device.h", "hc_internal.h", "hc_mfma_common.h", "hc_status.h", "hc_ffn.h", "hc_plan.h"]
+           "hc_ffn_api.cpp", "hc_norm.hip", "hc_gemm.hip",
+           "hc_attn_api.cpp", "hc_attn.hip", "hc_attn_bwd.hip", "hc_paged.hip"]
+HEADERS = ["hc_device.h", "hc_internal.h", "hc_mfma_common.h", "hc_status.h", "hc_ffn.h", "hc_plan.h", "hc_stage.h",
+           "hc_attn.h"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

@@ -1,0 +1,374 @@
+// Internal interfaces of the attention operators and the device parts that their kernels share.
+//
+// A sequence has q_len queries and k_len keys; query i stands at position p = i + k_len - q_len.
+// Query heads are G = heads / kv_heads to a key head, and the G heads of one query are
+// consecutive rows of one matrix: row r of a key head is query r / G, head r % G. So a tile of
+// rows reads every key once for all heads that share it.
+#pragma once
+
+#include "hc_ffn.h"
+#include "hc_stage.h"
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hc {
+
+struct Strides3 {
+  int64_t b, t, h;  // elements from one sequence, token and head to the next
+};
+
+struct AttnArgs {
+  const void *q, *k, *v;
+  void* out;                   // forward: written; backward: as saved
+  float* lse;                  // [rows of q][heads], natural logarithm; forward: or null
+  const int *q_starts, *k_starts;  // [batch + 1] of packed sequences, or null
+  Strides3 sq, sk, sv, so;
+  int64_t q_tokens, k_tokens;  // of a sequence; packed: of all
+  int batch, heads, kv_heads, group, dim;
+  int causal, window, sinks;   // window 0: none
+  float scale;
+  // backward
+  const void* d_out;
+  void *dq, *dk, *dv;
+  Strides3 sdo, sdq, sdk, sdv;
+  float* delta;                // [rows of q][heads]
+  // split over the keys
+  float* partial;
+  int splits;
+  int tiles;                   // row tiles (of a sequence; packed: at most, of all)
+};
+
+hipError_t launch_attention(AttnArgs a, int dtype, bool aligned, hipStream_t s);
+size_t attention_scratch(const AttnArgs& a, int dtype);
+hipError_t launch_attention_backward(AttnArgs a, int dtype, bool aligned, hipStream_t s);
+size_t attention_backward_scratch(const AttnArgs& a, int dtype);
+
+struct PagedArgs {
+  const void *q, *k, *v;  // k, v: the caches
+  void* out;
+  const int *table, *lengths;
+  Strides3 sq, sc, so;    // sc: page, row of a page, head (both caches); sq.b, so.b: sequence
+  int64_t table_stride;
+  int64_t pages;
+  int page, most_pages;   // rows of a page; entries of a sequence in the table
+  int batch, heads, kv_heads, group, dim;
+  int window, sinks;
+  float scale;
+  float* partial;
+  int splits, chunk;      // parts at most; keys of a part (a sequence longer than all parts has longer ones)
+};
+
+hipError_t launch_paged(PagedArgs a, int dtype, bool aligned, hipStream_t s);
+size_t paged_scratch(const PagedArgs& a, int dtype);
+
+struct StoreArgs {
+  const void *k, *v;
+  void *kc, *vc;
+  const int* slots;
+  Strides3 sk, sv, sc;    // t and h of the rows; page, row, head of the caches
+  int64_t tokens, pages;
+  int page, kv_heads, dim;
+};
+hipError_t launch_store(const StoreArgs& a, int dtype, bool aligned, hipStream_t s);
+
+struct MapArgs {
+  const int *cached, *fresh, *free_pages, *free_start;
+  int* table;
+  int64_t table_stride, tokens, free_count;
+  int batch, most_pages, page;
+  int *starts, *lengths, *positions, *slots, *taken;
+};
+hipError_t launch_page_map(const MapArgs& a, hipStream_t s);
+
+// ------------------------------------------------------------------ device parts
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float NEG_INF = -__builtin_inff();
+
+// D = A B + C with 32 x 32 results. 16-bit: contraction of 16, lane l holds A[l % 32][8 (l / 32) + 0..7]
+// and B[8 (l / 32) + 0..7][l % 32]; fp32: contraction of 8 in four ops, elements 4 (l / 32) + 0..3. Register r
+// of lane l is D[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].
+template <DT D> struct Piece { typedef s16x8 type; };
+template <> struct Piece<DT::F32> { typedef f32x4 type; };
+
+template <DT D> __device__ __forceinline__ f32x16 mfma32(typename Piece<D>::type a, typename Piece<D>::type b, f32x16 c) {
+  if constexpr (D == DT::BF16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  } else if constexpr (D == DT::F16) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+  }
+}
+
+// A tile of rows in LDS: 32 NB columns kept, each row PITCH of them apart, 16-byte chunks permuted inside a
+// row. Two kinds of reads have to spread over the 64 banks: 16 bytes of each of 32 consecutive rows (direct),
+// and 64 bytes of each of four consecutive rows (transposing). So the rows' low two bits move 64-byte
+// units, the next moves 32 bytes and the next 16, where neighbouring rows do not differ by themselves.
+template <DT D, int NB> struct Rows {
+  static constexpr int ES = D == DT::F32 ? 4 : 2, EPC = 16 / ES;
+  static constexpr int PITCH = NB <= 2 ? 64 : NB <= 4 ? 128 : 256;
+  static constexpr int RB = PITCH * ES, CPR = RB / 16;
+  static constexpr int STEP = D == DT::F32 ? 8 : 16;  // contraction of one piece
+  typedef typename Piece<D>::type piece;
+
+  static __device__ __forceinline__ int swz(int r) {
+    if constexpr (CPR >= 16) return ((r & 3) << 2) | ((r >> 1) & 2) | ((r >> 3) & 1);
+    else return ((r & 2) << 1) | ((r >> 1) & 2) | ((r >> 3) & 1);
+  }
+  // Piece of rows r0 .. r0+31 (r0 a multiple of 32) and columns STEP s ..: element r0 + l % 32 of either operand.
+  static __device__ __forceinline__ piece direct(const unsigned char* lds, int r0, int s, int lane) {
+    const int row = lane & 31, c = (lane >> 5) ^ swz(row);
+    return __builtin_bit_cast(piece, *(const uint4*)(lds + (r0 + row) * RB + ((c ^ (2 * s)) << 4)));
+  }
+  // Piece of columns 32 db .. 32 db + 31 over rows r0 .. r0+STEP-1, in the order of a 32 x 32 result's
+  // registers: 16-bit: elements 0..3 are rows r0 + 4 (l / 32) + 0..3, elements 4..7 eight rows further;
+  // fp32: rows r0 + 4 (l / 32) + 0..3.
+  static __device__ __forceinline__ piece transposed(const unsigned char* lds, int r0, int db, int lane) {
+    const int h = lane >> 5;
+    if constexpr (D == DT::F32) {
+      piece v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = r0 + 4 * h + e, c = (8 * db + ((lane & 31) >> 2)) ^ swz(row);
+        v[e] = *(const float*)(lds + row * RB + (c << 4) + 4 * (lane & 3));
+      }
+      return v;
+    } else {
+      const int j = lane & 15, row = r0 + 4 * h + (j >> 2);
+      const int c = 4 * db + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+      lds_u8* lo = (lds_u8*)(lds + row * RB + ((c ^ swz(row)) << 4) + 8 * (j & 1));
+      lds_u8* hi = (lds_u8*)(lds + (row + 8) * RB + ((c ^ swz(row + 8)) << 4) + 8 * (j & 1));
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)lo);
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)hi);
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+// Registers STEP-wise s of a 32 x 32 block of values (rows in registers) as a piece over those rows, rounded to T.
+template <DT D> __device__ __forceinline__ typename Piece<D>::type piece_of(const f32x16& x, int s) {
+  if constexpr (D == DT::F32) {
+    return f32x4{x[4 * s], x[4 * s + 1], x[4 * s + 2], x[4 * s + 3]};
+  } else {
+    const u32x4 w = {pack2<D>(x[8 * s], x[8 * s + 1]), pack2<D>(x[8 * s + 2], x[8 * s + 3]),
+                     pack2<D>(x[8 * s + 4], x[8 * s + 5]), pack2<D>(x[8 * s + 6], x[8 * s + 7])};
+    return __builtin_bit_cast(s16x8, w);
+  }
+}
+
+// Stages tiles of R rows by THREADS threads. Rows of the tile are rows of a tensor [tokens, heads, dim] at one
+// head (G = 1) or the packed rows of a key head's G heads.
+template <DT D, int NB, int R, int THREADS, bool ALN> struct Stager {
+  typedef Rows<D, NB> T;
+  static constexpr int NL = R * T::CPR / THREADS;  // chunks of a thread
+  static constexpr int BYTES = R * T::RB;
+  static_assert(R * T::CPR % THREADS == 0, "tile shape");
+  typedef typename Store<D>::type elem_t;
+
+  // Chunk i of this thread: its row in the tile and its columns.
+  static __device__ __forceinline__ int row(int i, int tid) { return (i * THREADS + tid) / T::CPR; }
+  static __device__ __forceinline__ int col(int i, int tid) {
+    const int r = row(i, tid);
+    return (((i * THREADS + tid) % T::CPR) ^ T::swz(r)) * T::EPC;
+  }
+  // Aligned: loads that write LDS. base: the tile's first row (the same in every lane); off(r): bytes of row r from there;
+  // n: rows that exist; the others, and columns from dim on, become zeros.
+  template <typename Off>
+  static __device__ __forceinline__ void load(const void* base, Off off, int n, int dim, uint32_t lds, int tid) {
+    static_assert(ALN, "aligned rows");
+    const u32x4 d = raw_desc(base);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int r = row(i, tid), c = col(i, tid);
+      const uint32_t o = r < n && c < dim ? off(r) + (uint32_t)(c * T::ES) : OUTSIDE;
+      lds_load<16, false>(d, o, __builtin_amdgcn_readfirstlane(lds + (i * THREADS + wave * 64) * 16));
+    }
+  }
+  // Rows at any address, through registers.
+  template <typename Off>
+  static __device__ __forceinline__ void fetch(const void* base, Off off, int n, int dim, int tid, uint4* v) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int r = row(i, tid), c = col(i, tid), left = dim - c;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < n && left > 0) {
+        const elem_t* p = (const elem_t*)((const char*)base + off(r)) + c;
+        if (left >= T::EPC) {
+          v[i] = ld16<D, false>(p);
+        } else {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int e = 0; e < T::EPC - 1; ++e)
+            if (e < left) {
+              if constexpr (D == DT::F32) w[e] = __float_as_uint(p[e]);
+              else w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+            }
+          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ void put(unsigned char* lds, int tid, const uint4* v) {
+#pragma unroll
+    for (int i = 0; i < NL; ++i) *(uint4*)(lds + (i * THREADS + tid) * 16) = v[i];
+  }
+};
+
+// Sixteen bytes of a row from column c on, zeros from dim on.
+template <DT D, bool ALN> __device__ __forceinline__ uint4 chunk16(const void* row, int c, int dim) {
+  constexpr int EPC = D == DT::F32 ? 4 : 8;
+  typedef typename Store<D>::type elem_t;
+  const elem_t* p = (const elem_t*)row + c;
+  if (c + EPC <= dim) return ld16<D, ALN>(p);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (!ALN && c < dim) {
+#pragma unroll
+    for (int e = 0; e < EPC - 1; ++e)
+      if (c + e < dim) {
+        if constexpr (D == DT::F32) w[e] = __float_as_uint(p[e]);
+        else w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+      }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Sixteen bytes to a row from column c on, columns from dim on left out.
+template <DT D, bool ALN> __device__ __forceinline__ void put_chunk16(void* row, int c, int dim, uint4 v) {
+  constexpr int EPC = D == DT::F32 ? 4 : 8;
+  typedef typename Store<D>::type elem_t;
+  elem_t* p = (elem_t*)row + c;
+  if (c + EPC <= dim) {
+    st16<D, ALN>(p, v);
+  } else if (!ALN && c < dim) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < EPC - 1; ++e)
+      if (c + e < dim) {
+        if constexpr (D == DT::F32) p[e] = __uint_as_float(w[e]);
+        else p[e] = (elem_t)(w[e >> 1] >> (16 * (e & 1)));
+      }
+  }
+}
+
+// The transposed result of a wave's 32 rows (row in the lane, columns 32 (d0 + d) .. in the registers of block d), times
+// f, rounded to T into LDS rows (32 of RB bytes, the wave's own).
+template <DT D, int NB, int N>
+__device__ __forceinline__ void rows_to_lds(unsigned char* lds, const f32x16 (&o)[N], float f, int lane) {
+  typedef Rows<D, NB> T;
+  const int row = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int col = 32 * d + 8 * u + 4 * h;
+      unsigned char* p = lds + row * T::RB + (((col / T::EPC) ^ T::swz(row)) << 4) + (col % T::EPC) * T::ES;
+      const float y0 = o[d][4 * u] * f, y1 = o[d][4 * u + 1] * f, y2 = o[d][4 * u + 2] * f, y3 = o[d][4 * u + 3] * f;
+      if constexpr (D == DT::F32) *(f32x4*)p = f32x4{y0, y1, y2, y3};
+      else *(u32x2*)p = u32x2{pack2<D>(y0, y1), pack2<D>(y2, y3)};
+    }
+}
+// 16 bytes of row `row` from column 16-byte chunk ch on, of rows that rows_to_lds wrote.
+template <DT D, int NB> __device__ __forceinline__ uint4 row_chunk(const unsigned char* lds, int row, int ch) {
+  typedef Rows<D, NB> T;
+  return *(const uint4*)(lds + row * T::RB + ((ch ^ T::swz(row)) << 4));
+}
+
+// The two halves' values of a wave combined: every lane gets f(x[l % 32], x[l % 32 + 32]).
+__device__ __forceinline__ float halves_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float halves_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Which keys a query sees: j with lo <= j <= hi or j < first.
+struct Sees {
+  int lo, hi, first;
+  __device__ __forceinline__ bool operator()(int j) const { return (j >= lo && j <= hi) || j < first; }
+};
+__device__ __forceinline__ Sees sees(const AttnArgs& a, int p, int k_len) {
+  Sees s;
+  const int last = a.causal ? min(p, k_len - 1) : k_len - 1;
+  s.hi = !a.causal && a.window ? min(last, p + a.window - 1) : last;
+  s.lo = a.window ? p - a.window + 1 : -(1 << 30);
+  s.first = a.window ? min(a.sinks, last + 1) : 0;
+  return s;
+}
+
+// The tiles of keys that a workgroup reads: [0, head) and [begin, end).
+struct KeyTiles {
+  int head, begin, count;
+  __device__ __forceinline__ int operator()(int i) const { return i < head ? i : i - head + begin; }
+};
+template <int KT> __device__ __forceinline__ KeyTiles key_tiles(const Sees& first_row, const Sees& last_row) {
+  // lo, hi and first ascend with the row (hi and first are constant where not causal).
+  KeyTiles t;
+  const int sink_tiles = (last_row.first + KT - 1) / KT;
+  t.begin = max(first_row.lo, 0) / KT;
+  int end = last_row.hi < 0 ? 0 : last_row.hi / KT + 1;
+  if (sink_tiles >= t.begin) {  // one range
+    end = max(end, sink_tiles);
+    t.begin = 0;
+    t.head = 0;
+  } else {
+    t.head = sink_tiles;
+  }
+  t.count = t.head + max(0, end - t.begin);
+  return t;
+}
+
+// The sequence of a workgroup and its place in it.
+struct Seq {
+  int64_t q0, k0;  // first rows
+  int b, ql, kl, tile;
+};
+// Packed sequences have tiles at floor(start * unit / TR) + b and after: at least as many as their rows
+// (unit to a token) need, in order, so the sequence of a tile is found by counting. Starts are held inside
+// the tensors whatever they say.
+__device__ __forceinline__ Seq find_sequence(const AttnArgs& a, const int* starts, int64_t tokens, int unit, int tr, int64_t t) {
+  Seq s;
+  if (!starts) {
+    s.b = (int)(t / a.tiles);
+    s.tile = (int)(t - (int64_t)s.b * a.tiles);
+    s.ql = (int)a.q_tokens;
+    s.kl = (int)a.k_tokens;
+    s.q0 = s.k0 = 0;  // the batch strides lead to the sequence
+    return s;
+  }
+  // 64 candidates at a time: the last sequence whose first tile is not after t.
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = a.batch;
+  while (n > 1) {
+    const int step = (n + 63) / 64, b = lo + lane * step;
+    bool in = false;
+    if (lane * step < n) {
+      const int64_t st = min(max((int64_t)starts[b], (int64_t)0), tokens);
+      in = st * unit / tr + b <= t;
+    }
+    // in is true up to some lane (tile numbers ascend where starts do); starts out of order give some sequence
+    const int c = __popcll(__ballot(in));
+    const int k = c > 0 ? c - 1 : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  s.b = __builtin_amdgcn_readfirstlane(lo);
+  auto at = [](const int* st, int i, int64_t most) { return min(max((int64_t)st[i], (int64_t)0), most); };
+  s.q0 = at(a.q_starts, s.b, a.q_tokens);
+  s.ql = (int)max((int64_t)0, at(a.q_starts, s.b + 1, a.q_tokens) - s.q0);
+  s.k0 = at(a.k_starts, s.b, a.k_tokens);
+  s.kl = (int)max((int64_t)0, at(a.k_starts, s.b + 1, a.k_tokens) - s.k0);
+  const int64_t st = starts == a.q_starts ? s.q0 : s.k0;
+  s.tile = (int)(t - (st * unit / tr + s.b));
+  return s;
+}
+
+}  // namespace hc

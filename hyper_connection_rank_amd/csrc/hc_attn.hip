@@ -1,0 +1,260 @@
+// Attention over whole sequences: hclrmix_attention.
+//
+// For a row r of queries, o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m) over the keys j that it sees, with
+// s_j = scale q.k_j. One pass over the keys: the running maximum m and the sums are kept in fp32 and the sums
+// scaled down when m grows. All exponentials are powers of two (scale log2 e is folded into one factor).
+//
+// The products are taken transposed: S^T = K Q^T has keys in a lane's registers and one query per lane, so the
+// maximum and the sum over keys are taken inside a lane (one exchange between the wave's halves), and the
+// registers of P^T are, rounded to T, the second operand of O^T = V^T P^T as they are: the contraction's
+// order is that of the registers, and the transposing LDS read gives V^T in the same order. P needs no LDS.
+#include "hc_attn.h"
+#include "hc_internal.h"
+
+#include <algorithm>
+
+namespace hc {
+
+template <DT D, int NB> struct FwdShape {
+  typedef Rows<D, NB> T;
+  static constexpr int KT = T::RB >= 1024 ? 32 : 64;  // keys of a tile: two buffers of K and V in at most 128 KB
+  static constexpr int WAVES = 4, QB = 1, TR = 32 * QB * WAVES;
+};
+
+// fp16 weights are taken 2^7 times as large, so that fewer of them fall below fp16's normal numbers; with the maximum up
+// to 2^8 behind (see below) they reach 2^15.
+template <DT D> constexpr float weight_shift() { return D == DT::F16 ? 7.0f : 0.0f; }
+constexpr float LAG = 8.0f;
+
+template <DT D, int NB, bool ALN>
+__global__ __launch_bounds__(256, 1) void k_attention(const AttnArgs a) {
+  typedef FwdShape<D, NB> F;
+  typedef Rows<D, NB> T;
+  typedef typename T::piece piece;
+  constexpr int KT = F::KT, KB = KT / 32, QB = F::QB, THREADS = 64 * F::WAVES;
+  constexpr int STEPS = 32 * NB / T::STEP;     // of a score
+  constexpr int PSTEPS = 32 / T::STEP;         // of 32 keys
+  typedef Stager<D, NB, KT, THREADS, ALN> S;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[4 * S::BYTES];
+  static_assert(F::WAVES * 32 * QB * T::RB <= 4 * S::BYTES, "the results fit the staging buffers");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+
+  // Workgroup -> key head and tile of rows. Consecutive ids go to the XCDs in turn: neighbouring heads to different
+  // ones, a head's tiles (which share its keys in an L2) to as few as there are. Late tiles first: with a causal
+  // mask they have the most keys.
+  const int kvh = blockIdx.x % a.kv_heads;
+  const int64_t t = (int64_t)(gridDim.x / a.kv_heads) - 1 - blockIdx.x / a.kv_heads;
+  const Seq s = find_sequence(a, a.q_starts, a.q_tokens, a.group, F::TR, t);
+  const int rows = s.ql * a.group, r0 = s.tile * F::TR;
+  if (s.tile < 0 || r0 >= rows) return;
+  const int64_t q_base = (a.q_starts ? s.q0 * a.sq.t : s.b * a.sq.b) + kvh * a.group * a.sq.h;
+  const char* kp = (const char*)a.k + ((a.k_starts ? s.k0 * a.sk.t : s.b * a.sk.b) + kvh * a.sk.h) * T::ES;
+  const char* vp = (const char*)a.v + ((a.k_starts ? s.k0 * a.sv.t : s.b * a.sv.b) + kvh * a.sv.h) * T::ES;
+  const int off = s.kl - s.ql;
+
+  // This lane's queries and what they see; rows past the last one repeat it and are not written.
+  piece q[QB][STEPS];
+  Sees see[QB];
+#pragma unroll
+  for (int b = 0; b < QB; ++b) {
+    const int r = min(r0 + (wave * QB + b) * 32 + (lane & 31), rows - 1), tok = r / a.group, g = r - tok * a.group;
+    const char* p = (const char*)a.q + (q_base + tok * a.sq.t + g * a.sq.h) * T::ES;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) q[b][i] = __builtin_bit_cast(piece, chunk16<D, ALN>(p, (2 * i + h) * T::EPC, a.dim));
+    see[b] = sees(a, tok + off, s.kl);
+  }
+  const Sees wg_first = sees(a, r0 / a.group + off, s.kl);
+  const Sees wg_last = sees(a, min(r0 + F::TR - 1, rows - 1) / a.group + off, s.kl);
+  const KeyTiles tiles = key_tiles<KT>(wg_first, wg_last);
+  const Sees w_first = sees(a, min(r0 + wave * QB * 32, rows - 1) / a.group + off, s.kl);
+  const Sees w_last = sees(a, min(r0 + (wave * QB + QB) * 32 - 1, rows - 1) / a.group + off, s.kl);
+
+  f32x16 o[QB][NB];
+  float m[QB], l[QB];
+#pragma unroll
+  for (int b = 0; b < QB; ++b) {
+#pragma unroll
+    for (int d = 0; d < NB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[b][d][e] = 0.0f;
+    m[b] = NEG_INF;
+    l[b] = 0.0f;
+  }
+  const float c = a.scale * LOG2E;
+
+  auto multiply = [&](const unsigned char* kt, const unsigned char* vt, int j0) {
+    // Nothing of this tile is seen by this wave's rows, or everything by all.
+    const int j1 = j0 + KT - 1;
+    if (j0 > max(w_last.hi, w_last.first - 1) || (j1 < w_first.lo && j0 >= w_last.first)) return;
+    const bool whole = (j0 >= w_last.lo && j1 <= w_first.hi) || j1 < w_first.first;
+    f32x16 x[KB][QB];
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int b = 0; b < QB; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[k][b][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        const piece f = T::direct(kt, 32 * k, i, lane);
+#pragma unroll
+        for (int b = 0; b < QB; ++b) x[k][b] = mfma32<D>(f, q[b][i], x[k][b]);
+      }
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      if (!whole) {
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            x[k][b][e] = see[b](j0 + 32 * k + 8 * (e >> 2) + 4 * h + (e & 3)) ? x[k][b][e] : NEG_INF;
+      }
+      float top = x[0][b][0];
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, x[k][b][e]);
+      top = halves_max(top) * c;
+      // The sums are scaled down only when the maximum has grown by more than 2^LAG since: until then the weights
+      // are at most 2^LAG, which fp32 sums (and T) hold as well.
+      if (__ballot(top > m[b] + LAG)) {
+        const float grown = fmaxf(m[b], top);
+        const float f = grown == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(m[b] - grown);
+        m[b] = grown;
+        l[b] *= f;
+#pragma unroll
+        for (int d = 0; d < NB; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[b][d][e] *= f;
+      }
+      const float base = weight_shift<D>() - (m[b] == NEG_INF ? 0.0f : m[b]);
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[k][b][e] = __builtin_amdgcn_exp2f(fmaf(x[k][b][e], c, base));
+          l[b] += x[k][b][e];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int i = 0; i < PSTEPS; ++i) {
+        piece p[QB];
+#pragma unroll
+        for (int b = 0; b < QB; ++b) p[b] = piece_of<D>(x[k][b], i);
+#pragma unroll
+        for (int d = 0; d < NB; ++d) {
+          const piece f = T::transposed(vt, 32 * k + T::STEP * i, d, lane);
+#pragma unroll
+          for (int b = 0; b < QB; ++b) o[b][d] = mfma32<D>(f, p[b], o[b][d]);
+        }
+      }
+  };
+
+  const uint32_t ldk = (uint32_t)(a.sk.t * T::ES), ldv = (uint32_t)(a.sv.t * T::ES);
+  auto k_at = [&](int j0) { return kp + (int64_t)j0 * a.sk.t * T::ES; };
+  auto v_at = [&](int j0) { return vp + (int64_t)j0 * a.sv.t * T::ES; };
+  auto k_off = [&](int r) { return (uint32_t)r * ldk; };
+  auto v_off = [&](int r) { return (uint32_t)r * ldv; };
+  if constexpr (ALN) {
+    const uint32_t l0 = lds_offset(lds);
+    auto stage = [&](int i) {
+      const int j0 = tiles(i) * KT, n = s.kl - j0;
+      const uint32_t to = l0 + (i & 1) * 2 * S::BYTES;
+      S::load(k_at(j0), k_off, n, a.dim, to, tid);
+      S::load(v_at(j0), v_off, n, a.dim, to + S::BYTES, tid);
+    };
+    if (tiles.count > 0) stage(0);
+    for (int i = 0; i < tiles.count; ++i) {
+      // Tile i has arrived, and every wave is done with tile i - 1, whose buffer tile i + 1 fills.
+      wait_loads<0>();
+      lds_barrier();
+      if (i + 1 < tiles.count) stage(i + 1);
+      const unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
+      multiply(cur, cur + S::BYTES, tiles(i) * KT);
+    }
+  } else {
+    uint4 fk[S::NL], fv[S::NL];
+    auto fetch = [&](int i) {
+      const int j0 = tiles(i) * KT, n = s.kl - j0;
+      S::fetch(k_at(j0), k_off, n, a.dim, tid, fk);
+      S::fetch(v_at(j0), v_off, n, a.dim, tid, fv);
+    };
+    if (tiles.count > 0) fetch(0);
+    for (int i = 0; i < tiles.count; ++i) {
+      unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
+      S::put(cur, tid, fk);
+      S::put(cur + S::BYTES, tid, fv);
+      lds_barrier();
+      if (i + 1 < tiles.count) fetch(i + 1);
+      multiply(cur, cur + S::BYTES, tiles(i) * KT);
+    }
+  }
+  lds_barrier();
+
+  // O^T through LDS (each wave its own part), so that rows are written 16 bytes a lane.
+#pragma unroll
+  for (int b = 0; b < QB; ++b) {
+    const float total = halves_sum(l[b]), inv = total == 0.0f ? 0.0f : 1.0f / total;
+    rows_to_lds<D, NB>(lds + (wave * QB + b) * 32 * T::RB, o[b], inv, lane);
+    const int row = lane & 31;
+    const int first = r0 + (wave * QB + b) * 32;
+    if (a.lse && lane < 32 && first + row < rows) {
+      const int r = first + row, tok = r / a.group;
+      const int64_t at = ((a.q_starts ? s.q0 : s.b * a.q_tokens) + tok) * a.heads + kvh * a.group + r - tok * a.group;
+      a.lse[at] = total == 0.0f ? NEG_INF : (m[b] - weight_shift<D>() + __builtin_amdgcn_logf(total)) * LN2;
+    }
+  }
+  lds_barrier();
+  const int64_t o_base = (a.q_starts ? s.q0 * a.so.t : s.b * a.so.b) + kvh * a.group * a.so.h;
+#pragma unroll 4
+  for (int i = lane; i < QB * 32 * T::CPR; i += 64) {
+    const int row = i / T::CPR, r = r0 + wave * QB * 32 + row, ch = i % T::CPR;
+    if (r >= rows) continue;
+    const int tok = r / a.group, g = r - tok * a.group;
+    const uint4 v = row_chunk<D, NB>(lds + wave * QB * 32 * T::RB, row, ch);
+    put_chunk16<D, ALN>((char*)a.out + (o_base + tok * a.so.t + g * a.so.h) * T::ES, ch * T::EPC, a.dim, v);
+  }
+}
+
+namespace {
+
+template <DT D, int NB> hipError_t go(const AttnArgs& a0, bool aligned, hipStream_t s) {
+  typedef FwdShape<D, NB> F;
+  AttnArgs a = a0;
+  const int64_t rows = a.q_tokens * a.group;
+  int64_t tiles;
+  if (a.q_starts) tiles = rows / F::TR + a.batch;
+  else {
+    a.tiles = (int)((rows + F::TR - 1) / F::TR);
+    tiles = (int64_t)a.tiles * a.batch;
+  }
+  const dim3 grid((unsigned)(tiles * a.kv_heads)), block(64 * F::WAVES);
+  if (aligned) hipLaunchKernelGGL((k_attention<D, NB, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_attention<D, NB, false>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+template <DT D> hipError_t go_dim(const AttnArgs& a, bool aligned, hipStream_t s) {
+  if (a.dim <= 64) return go<D, 2>(a, aligned, s);
+  if (a.dim <= 96) return go<D, 3>(a, aligned, s);
+  if (a.dim <= 128) return go<D, 4>(a, aligned, s);
+  return go<D, 8>(a, aligned, s);
+}
+
+}  // namespace
+
+hipError_t launch_attention(AttnArgs a, int dtype, bool aligned, hipStream_t s) {
+  switch (dtype) {
+    case (int)DT::F32: return go_dim<DT::F32>(a, aligned, s);
+    case (int)DT::F16: return go_dim<DT::F16>(a, aligned, s);
+    default: return go_dim<DT::BF16>(a, aligned, s);
+  }
+}
+
+size_t attention_scratch(const AttnArgs&, int) { return 0; }
+
+}  // namespace hc

@@ -1,0 +1,492 @@
+// C entry points of the attention operators (attention, paged_attention, cache_store, page_map): validation,
+// workspace layout and launches. Everything is checked on the host before anything is enqueued; what only the device
+// knows (starts, tables, lengths, slots) is held inside the tensors by the kernels.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <initializer_list>
+
+#include "hc_attn.h"
+#include "hc_internal.h"
+#include "hc_status.h"
+
+namespace {
+
+using hc::fail;
+using hc::ok;
+
+constexpr int64_t MAX_STRIDE = int64_t(1) << 21;  // elements between tokens: a tile's offsets fit 31 bits
+constexpr int64_t MAX_SPAN = int64_t(1) << 40;    // elements between sequences, heads or pages
+
+size_t elem_size(int dtype) { return dtype == HCLRMIX_F32 ? 4 : 2; }
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+hclrmix_status done(hipError_t e) {
+  return e == hipSuccess ? ok() : fail(HCLRMIX_ERR_DEVICE, "HIP error: %s", hipGetErrorString(e));
+}
+
+// One tensor of a call: rows of `len` elements at three strides.
+struct View {
+  const char* name;
+  const void* p;
+  int64_t n[3], s[3];  // sequences (or pages), tokens, heads
+  int64_t len;
+  bool output;
+  size_t es;
+  bool given() const { return p != nullptr && n[0] > 0 && n[1] > 0 && n[2] > 0; }
+  uintptr_t lo() const { return (uintptr_t)p; }
+  uintptr_t hi() const {
+    int64_t last = len;
+    for (int i = 0; i < 3; ++i) last += (n[i] - 1) * s[i];
+    return lo() + (size_t)last * es;
+  }
+};
+
+// Strides of a tensor [n0][n1][n2][len]: 0 counts as contiguous. Dimensions of one element take part in nothing.
+hclrmix_status view(View& v, const char* name, const void* p, const hclrmix_strides& st, int64_t n0, int64_t n1, int64_t n2, int64_t len,
+                    size_t es, bool output) {
+  v = View{name, p, {n0, n1, n2}, {0, 0, 0}, len, output, es};
+  if (st.sequence < 0 || st.token < 0 || st.head < 0)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "%s has a negative stride", name);
+  v.s[2] = st.head ? st.head : len;
+  v.s[1] = st.token ? st.token : n2 * (st.head ? st.head : len);
+  v.s[0] = st.sequence ? st.sequence : n1 * v.s[1];
+  for (int i = 0; i < 3; ++i)
+    if (v.n[i] <= 1) v.s[i] = 0;
+  if (v.s[1] > MAX_STRIDE) return fail(HCLRMIX_ERR_UNSUPPORTED, "%s: strides between tokens are at most 2^21", name);
+  if (v.s[0] > MAX_SPAN || v.s[2] > MAX_SPAN) return fail(HCLRMIX_ERR_UNSUPPORTED, "%s: strides are at most 2^40", name);
+  if (p && (uintptr_t)p % es) return fail(HCLRMIX_ERR_UNSUPPORTED, "%s must be element-aligned", name);
+  // Rows of one tensor must not lie on each other: every stride, in ascending order, clears what the smaller ones span.
+  if (n0 == 0 || n1 == 0 || n2 == 0) return HCLRMIX_OK;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return v.s[a] < v.s[b]; });
+  int64_t span = len;
+  for (int i : order) {
+    if (v.n[i] <= 1) continue;
+    if (v.s[i] < span) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "%s: rows overlap", name);
+    span += (v.n[i] - 1) * v.s[i];
+  }
+  return HCLRMIX_OK;
+}
+
+// Tensors that share no byte: their ranges are apart, or both are columns of the rows of one matrix (as q, k and v are
+// of a merged projection), in ranges that are apart.
+bool apart(const View& a, const View& b) {
+  if (a.hi() <= b.lo() || b.hi() <= a.lo()) return true;
+  const int64_t row = a.s[1] ? a.s[1] : b.s[1];
+  if (row == 0 || (a.s[1] && a.s[1] != row) || (b.s[1] && b.s[1] != row)) return false;
+  if (a.s[0] % row || b.s[0] % row || a.es != b.es) return false;
+  const int64_t wa = (a.n[2] - 1) * a.s[2] + a.len, wb = (b.n[2] - 1) * b.s[2] + b.len;
+  if (wa > row || wb > row) return false;
+  const int64_t bytes = row * (int64_t)a.es;
+  const int64_t d = ((int64_t)(b.lo() - a.lo()) % bytes + bytes) % bytes;
+  return d >= wa * (int64_t)a.es && d + wb * (int64_t)a.es <= bytes;
+}
+
+// A plain range (starts, statistics, a workspace) as a view of one row of bytes.
+View range(const char* name, const void* p, size_t bytes, bool output) {
+  return View{name, p, {1, 1, 1}, {0, 0, 0}, (int64_t)bytes, output, 1};
+}
+
+hclrmix_status check_apart(std::initializer_list<const View*> all) {
+  for (const View* o : all) {
+    if (!o->given() || !o->output || o->len == 0) continue;
+    for (const View* i : all)
+      if (i != o && i->given() && i->len > 0 && !apart(*o, *i))
+        return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "%s overlaps %s", o->name, i->name);
+  }
+  return HCLRMIX_OK;
+}
+
+// Whether every row starts on 16 bytes and is whole chunks of 16.
+bool aligned16(std::initializer_list<const View*> all) {
+  for (const View* v : all) {
+    if (!v->p) continue;
+    uintptr_t x = (uintptr_t)v->p | (uintptr_t)(v->len * (int64_t)v->es);
+    for (int i = 0; i < 3; ++i) x |= (uintptr_t)(v->s[i] * (int64_t)v->es);
+    if (x & 15u) return false;
+  }
+  return true;
+}
+
+hc::Strides3 strides(const View& v) { return {v.s[0], v.s[1], v.s[2]}; }
+
+hclrmix_status check_ints(const char* name, const void* p) {
+  return (uintptr_t)p & 3u ? fail(HCLRMIX_ERR_UNSUPPORTED, "%s must be 4-byte aligned", name) : HCLRMIX_OK;
+}
+
+hclrmix_status check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return HCLRMIX_OK;
+  if (!ws || bytes < need) return fail(HCLRMIX_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes, got %zu", need, bytes);
+  if ((uintptr_t)ws & 15u) return fail(HCLRMIX_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+  return HCLRMIX_OK;
+}
+
+// What the operators have in common: element type, heads and head size, window, first tokens and scale.
+hclrmix_status check_heads(int dtype, int heads, int kv_heads, int dim) {
+  if (dtype != HCLRMIX_F32 && dtype != HCLRMIX_F16 && dtype != HCLRMIX_BF16)
+    return fail(HCLRMIX_ERR_UNSUPPORTED, "unknown dtype %d", dtype);
+  if (heads < 1 || kv_heads < 1 || dim < 1) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "heads, kv_heads and dim must be >= 1");
+  if (heads % kv_heads) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "heads must be a multiple of kv_heads");
+  if (heads > HCLRMIX_ATTENTION_MAX_HEADS || dim > HCLRMIX_ATTENTION_MAX_DIM)
+    return fail(HCLRMIX_ERR_UNSUPPORTED, "at most %d heads of %d", HCLRMIX_ATTENTION_MAX_HEADS, HCLRMIX_ATTENTION_MAX_DIM);
+  return HCLRMIX_OK;
+}
+hclrmix_status check_mask(int window, int sinks, float scale) {
+  if (window < 0 || sinks < 0) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "window and sinks must be >= 0");
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "scale must be finite and positive");
+  return HCLRMIX_OK;
+}
+// Positions are below 2^30: a window or sinks from there on hold every key.
+int held(int x) { return std::min(x, 1 << 29); }
+
+hclrmix_status check_attention(const hclrmix_attention_problem* p) {
+  if (!p) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem must not be NULL");
+  if (p->reserved[0] || p->reserved[1]) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem.reserved must be 0");
+  if (hclrmix_status st = check_heads(p->dtype, p->heads, p->kv_heads, p->dim)) return st;
+  if (hclrmix_status st = check_mask(p->window, p->sinks, p->scale)) return st;
+  if (p->causal < 0 || p->causal > 1 || p->packed < 0 || p->packed > 1)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "causal and packed must be 0 or 1");
+  if (p->batch < 0 || p->q_tokens < 0 || p->k_tokens < 0)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "batch and tokens must be >= 0");
+  if (p->batch > HCLRMIX_ATTENTION_MAX_BATCH || p->q_tokens > HCLRMIX_MAX_ROWS || p->k_tokens > HCLRMIX_MAX_ROWS)
+    return fail(HCLRMIX_ERR_UNSUPPORTED, "at most %d sequences and %d tokens", HCLRMIX_ATTENTION_MAX_BATCH, HCLRMIX_MAX_ROWS);
+  // Row tiles of every kernel stay inside a launch's grid, and a sequence's rows inside 31 bits.
+  const int64_t n = p->packed ? 1 : p->batch;
+  if (std::max(n * p->q_tokens, n * p->k_tokens) * p->heads > (int64_t(1) << 29) || p->batch * p->heads > (int64_t(1) << 20))
+    return fail(HCLRMIX_ERR_UNSUPPORTED, "tokens x heads are at most 2^29, batch x heads 2^20");
+  return HCLRMIX_OK;
+}
+
+hc::AttnArgs attention_args(const hclrmix_attention_problem* p) {
+  hc::AttnArgs a{};
+  a.q_tokens = p->q_tokens;
+  a.k_tokens = p->k_tokens;
+  a.batch = (int)p->batch;
+  a.heads = p->heads;
+  a.kv_heads = p->kv_heads;
+  a.group = p->heads / p->kv_heads;
+  a.dim = p->dim;
+  a.causal = p->causal;
+  a.window = held(p->window);
+  a.sinks = held(p->sinks);
+  a.scale = p->scale;
+  a.splits = 1;
+  return a;
+}
+
+size_t attention_need(const hclrmix_attention_problem* p) {
+  hc::AttnArgs a = attention_args(p);
+  a.q_starts = p->packed ? (const int*)4 : nullptr;  // only told from NULL
+  return HCLRMIX_COUNTER_BYTES + up256(hc::attention_scratch(a, p->dtype));
+}
+size_t attention_backward_need(const hclrmix_attention_problem* p) {
+  hc::AttnArgs a = attention_args(p);
+  a.q_starts = p->packed ? (const int*)4 : nullptr;
+  return HCLRMIX_COUNTER_BYTES + up256(hc::attention_backward_scratch(a, p->dtype));
+}
+
+// Sequences and tokens of one as the tensors have them: packed, one sequence of all.
+struct Extent {
+  int64_t n, q, k;
+};
+Extent extent(const hclrmix_attention_problem& p) { return {p.packed ? 1 : p.batch, p.q_tokens, p.k_tokens}; }
+
+hclrmix_status check_starts(const hclrmix_attention_problem& p, const int32_t* q_starts, const int32_t* k_starts) {
+  if (p.packed ? !q_starts : q_starts != nullptr || k_starts != nullptr)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "starts do not match problem.packed");
+  if (p.packed && !k_starts && p.q_tokens != p.k_tokens)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "k_starts may be left out only where q and k have the same rows");
+  if (hclrmix_status st = check_ints("q_starts", q_starts)) return st;
+  return check_ints("k_starts", k_starts);
+}
+
+hclrmix_status check_paged(const hclrmix_paged_problem* p) {
+  if (!p) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem must not be NULL");
+  if (p->reserved) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem.reserved must be 0");
+  if (hclrmix_status st = check_heads(p->dtype, p->heads, p->kv_heads, p->dim)) return st;
+  if (hclrmix_status st = check_mask(p->window, p->sinks, p->scale)) return st;
+  if (p->batch < 0 || p->pages < 0 || p->most_pages < 0 || p->page_size < 1 || p->table_stride < 0)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "batch, pages and most_pages must be >= 0, page_size >= 1");
+  if (p->table_stride && p->table_stride < p->most_pages)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "table_stride is shorter than a row of the table");
+  if (p->batch > HCLRMIX_ATTENTION_MAX_BATCH || p->batch * p->heads > (int64_t(1) << 20))
+    return fail(HCLRMIX_ERR_UNSUPPORTED, "at most %d sequences, batch x heads at most 2^20", HCLRMIX_ATTENTION_MAX_BATCH);
+  if (p->page_size > HCLRMIX_MAX_PAGE_SIZE || p->pages > INT32_MAX || p->most_pages > INT32_MAX ||
+      p->most_pages * p->page_size > (int64_t(1) << 29) || p->table_stride > MAX_SPAN)
+    return fail(HCLRMIX_ERR_UNSUPPORTED, "pages are at most %d rows, a sequence's table at most 2^29 tokens", HCLRMIX_MAX_PAGE_SIZE);
+  return HCLRMIX_OK;
+}
+
+hc::PagedArgs paged_args(const hclrmix_paged_problem* p) {
+  hc::PagedArgs a{};
+  a.table_stride = p->table_stride ? p->table_stride : p->most_pages;
+  a.pages = p->pages;
+  a.page = (int)p->page_size;
+  a.most_pages = (int)p->most_pages;
+  a.batch = (int)p->batch;
+  a.heads = p->heads;
+  a.kv_heads = p->kv_heads;
+  a.group = p->heads / p->kv_heads;
+  a.dim = p->dim;
+  a.window = held(p->window);
+  a.sinks = held(p->sinks);
+  if (!a.window) a.sinks = 0;
+  a.scale = p->scale;
+  return a;
+}
+
+size_t paged_need(const hclrmix_paged_problem* p) {
+  return HCLRMIX_COUNTER_BYTES + up256(hc::paged_scratch(paged_args(p), p->dtype));
+}
+
+}  // namespace
+
+extern "C" {
+
+hclrmix_status hclrmix_attention_workspace_size(const hclrmix_attention_problem* problem, size_t* bytes) {
+  if (hclrmix_status st = check_attention(problem)) return st;
+  if (!bytes) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "bytes must not be NULL");
+  *bytes = attention_need(problem);
+  return ok();
+}
+
+hclrmix_status hclrmix_attention_backward_workspace_size(const hclrmix_attention_problem* problem, size_t* bytes) {
+  if (hclrmix_status st = check_attention(problem)) return st;
+  if (!bytes) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "bytes must not be NULL");
+  *bytes = attention_backward_need(problem);
+  return ok();
+}
+
+hclrmix_status hclrmix_attention(const void* q, const void* k, const void* v, const int32_t* q_starts,
+                                 const int32_t* k_starts, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, const hclrmix_attention_problem* problem, void* stream) {
+  if (hclrmix_status st = check_attention(problem)) return st;
+  const hclrmix_attention_problem& p = *problem;
+  if (hclrmix_status st = check_starts(p, q_starts, k_starts)) return st;
+  const size_t es = elem_size(p.dtype);
+  const Extent e = extent(p);
+  View vq, vk, vv, vo;
+  if (hclrmix_status st = view(vq, "q", q, p.q, e.n, e.q, p.heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vk, "k", k, p.k, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vv, "v", v, p.v, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vo, "out", out, p.out, e.n, e.q, p.heads, p.dim, es, true)) return st;
+  if (p.batch == 0 || p.q_tokens == 0) return ok();
+  if (!q || !out || (p.k_tokens > 0 && (!k || !v)))
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "q, k, v and out are required");
+  if ((uintptr_t)lse & 3u) return fail(HCLRMIX_ERR_UNSUPPORTED, "lse must be element-aligned");
+  const size_t need = attention_need(problem);
+  const View vs = range("q_starts", q_starts, 4 * (p.batch + 1), false), vt = range("k_starts", k_starts, 4 * (p.batch + 1), false),
+             vl = range("lse", lse, 4 * (size_t)(e.n * e.q * p.heads), true), vw = range("workspace", workspace, std::min(need, workspace_bytes), true);
+  if (hclrmix_status st = check_apart({&vq, &vk, &vv, &vo, &vs, &vt, &vl, &vw})) return st;
+  if (hclrmix_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  hc::AttnArgs a = attention_args(problem);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse;
+  a.q_starts = q_starts;
+  a.k_starts = k_starts ? k_starts : q_starts;
+  a.sq = strides(vq);
+  a.sk = strides(vk);
+  a.sv = strides(vv);
+  a.so = strides(vo);
+  a.partial = (float*)((char*)workspace + HCLRMIX_COUNTER_BYTES);
+  (void)hipGetLastError();
+  return done(hc::launch_attention(a, p.dtype, aligned16({&vq, &vk, &vv, &vo}), (hipStream_t)stream));
+}
+
+hclrmix_status hclrmix_attention_backward(const void* q, const void* k, const void* v, const void* out,
+                                          const float* lse, const void* d_out, const int32_t* q_starts,
+                                          const int32_t* k_starts, void* dq, void* dk, void* dv, void* workspace,
+                                          size_t workspace_bytes, const hclrmix_attention_problem* problem,
+                                          void* stream) {
+  if (hclrmix_status st = check_attention(problem)) return st;
+  const hclrmix_attention_problem& p = *problem;
+  if (hclrmix_status st = check_starts(p, q_starts, k_starts)) return st;
+  if (!dq && !dk && !dv) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "no gradient is wanted");
+  const size_t es = elem_size(p.dtype);
+  const Extent e = extent(p);
+  View vq, vk, vv, vo, vg, wq, wk, wv;
+  if (hclrmix_status st = view(vq, "q", q, p.q, e.n, e.q, p.heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vk, "k", k, p.k, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vv, "v", v, p.v, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vo, "out", out, p.out, e.n, e.q, p.heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vg, "d_out", d_out, p.d_out, e.n, e.q, p.heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(wq, "dq", dq, p.dq, e.n, e.q, p.heads, p.dim, es, true)) return st;
+  if (hclrmix_status st = view(wk, "dk", dk, p.dk, e.n, e.k, p.kv_heads, p.dim, es, true)) return st;
+  if (hclrmix_status st = view(wv, "dv", dv, p.dv, e.n, e.k, p.kv_heads, p.dim, es, true)) return st;
+  if (p.batch == 0 || (p.q_tokens == 0 && p.k_tokens == 0)) return ok();
+  if ((p.q_tokens > 0 && (!q || !out || !d_out || !lse)) || (p.k_tokens > 0 && (!k || !v)))
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "q, k, v, out, lse and d_out are required");
+  if ((uintptr_t)lse & 3u) return fail(HCLRMIX_ERR_UNSUPPORTED, "lse must be element-aligned");
+  const size_t need = attention_backward_need(problem);
+  const View vs = range("q_starts", q_starts, 4 * (p.batch + 1), false), vt = range("k_starts", k_starts, 4 * (p.batch + 1), false),
+             vl = range("lse", lse, 4 * (size_t)(e.n * e.q * p.heads), false), vw = range("workspace", workspace, std::min(need, workspace_bytes), true);
+  if (hclrmix_status st = check_apart({&vq, &vk, &vv, &vo, &vg, &wq, &wk, &wv, &vs, &vt, &vl, &vw})) return st;
+  if (hclrmix_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  hc::AttnArgs a = attention_args(problem);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = const_cast<void*>(out);
+  a.lse = const_cast<float*>(lse);
+  a.d_out = d_out;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.q_starts = q_starts;
+  a.k_starts = k_starts ? k_starts : q_starts;
+  a.sq = strides(vq);
+  a.sk = strides(vk);
+  a.sv = strides(vv);
+  a.so = strides(vo);
+  a.sdo = strides(vg);
+  a.sdq = strides(wq);
+  a.sdk = strides(wk);
+  a.sdv = strides(wv);
+  a.delta = (float*)((char*)workspace + HCLRMIX_COUNTER_BYTES);
+  (void)hipGetLastError();
+  return done(hc::launch_attention_backward(a, p.dtype, aligned16({&vq, &vk, &vv, &vo, &vg, &wq, &wk, &wv}), (hipStream_t)stream));
+}
+
+hclrmix_status hclrmix_paged_attention_workspace_size(const hclrmix_paged_problem* problem, size_t* bytes) {
+  if (hclrmix_status st = check_paged(problem)) return st;
+  if (!bytes) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "bytes must not be NULL");
+  *bytes = paged_need(problem);
+  return ok();
+}
+
+hclrmix_status hclrmix_paged_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* table,
+                                       const int32_t* lengths, void* out, void* workspace, size_t workspace_bytes,
+                                       const hclrmix_paged_problem* problem, void* stream) {
+  if (hclrmix_status st = check_paged(problem)) return st;
+  const hclrmix_paged_problem& p = *problem;
+  const size_t es = elem_size(p.dtype);
+  View vq, vk, vv, vo;
+  if (hclrmix_status st = view(vq, "q", q, p.q, p.batch, 1, p.heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vk, "k_cache", k_cache, p.cache, p.pages, p.page_size, p.kv_heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vv, "v_cache", v_cache, p.cache, p.pages, p.page_size, p.kv_heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vo, "out", out, p.out, p.batch, 1, p.heads, p.dim, es, true)) return st;
+  if (p.batch == 0) return ok();
+  if (!q || !out || !lengths || (p.most_pages > 0 && !table) || (p.pages > 0 && (!k_cache || !v_cache)))
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "q, k_cache, v_cache, table, lengths and out are required");
+  if (hclrmix_status st = check_ints("table", table)) return st;
+  if (hclrmix_status st = check_ints("lengths", lengths)) return st;
+  const size_t need = paged_need(problem);
+  hc::PagedArgs a = paged_args(problem);
+  const View vt = range("table", table, p.most_pages ? 4 * (size_t)((p.batch - 1) * a.table_stride + p.most_pages) : 0, false),
+             vl = range("lengths", lengths, 4 * (size_t)p.batch, false), vw = range("workspace", workspace, std::min(need, workspace_bytes), true);
+  if (hclrmix_status st = check_apart({&vq, &vk, &vv, &vo, &vt, &vl, &vw})) return st;
+  if (hclrmix_status st = check_workspace(workspace, workspace_bytes, need)) return st;
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.out = out;
+  a.table = table;
+  a.lengths = lengths;
+  a.sq = strides(vq);
+  a.sc = strides(vk);
+  a.so = strides(vo);
+  a.partial = (float*)((char*)workspace + HCLRMIX_COUNTER_BYTES);
+  (void)hipGetLastError();
+  return done(hc::launch_paged(a, p.dtype, aligned16({&vq, &vk, &vv, &vo}), (hipStream_t)stream));
+}
+
+hclrmix_status hclrmix_cache_store(const void* k, const void* v, const int32_t* slots, void* k_cache, void* v_cache,
+                                   const hclrmix_store_problem* problem, void* stream) {
+  if (!problem) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem must not be NULL");
+  const hclrmix_store_problem& p = *problem;
+  if (hclrmix_status st = check_heads(p.dtype, p.kv_heads, p.kv_heads, p.dim)) return st;
+  if (p.reserved) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem.reserved must be 0");
+  if (p.tokens < 0 || p.pages < 0 || p.page_size < 1)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "tokens and pages must be >= 0, page_size >= 1");
+  if (p.tokens > HCLRMIX_MAX_ROWS || p.page_size > HCLRMIX_MAX_PAGE_SIZE || p.pages > INT32_MAX)
+    return fail(HCLRMIX_ERR_UNSUPPORTED, "at most %d tokens, pages of at most %d rows", HCLRMIX_MAX_ROWS, HCLRMIX_MAX_PAGE_SIZE);
+  const size_t es = elem_size(p.dtype);
+  View vk, vv, ck, cv;
+  if (hclrmix_status st = view(vk, "k", k, p.k, 1, p.tokens, p.kv_heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(vv, "v", v, p.v, 1, p.tokens, p.kv_heads, p.dim, es, false)) return st;
+  if (hclrmix_status st = view(ck, "k_cache", k_cache, p.cache, p.pages, p.page_size, p.kv_heads, p.dim, es, true)) return st;
+  if (hclrmix_status st = view(cv, "v_cache", v_cache, p.cache, p.pages, p.page_size, p.kv_heads, p.dim, es, true)) return st;
+  if (p.tokens == 0 || p.pages == 0) return ok();
+  if (!k || !v || !slots || !k_cache || !v_cache)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "k, v, slots, k_cache and v_cache are required");
+  if (hclrmix_status st = check_ints("slots", slots)) return st;
+  const View vs = range("slots", slots, 4 * (size_t)p.tokens, false);
+  if (hclrmix_status st = check_apart({&vk, &vv, &ck, &cv, &vs})) return st;
+  hc::StoreArgs a{};
+  a.k = k;
+  a.v = v;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.slots = slots;
+  a.sk = strides(vk);
+  a.sv = strides(vv);
+  a.sc = strides(ck);
+  a.tokens = p.tokens;
+  a.pages = p.pages;
+  a.page = (int)p.page_size;
+  a.kv_heads = p.kv_heads;
+  a.dim = p.dim;
+  (void)hipGetLastError();
+  return done(hc::launch_store(a, p.dtype, aligned16({&vk, &vv, &ck, &cv}), (hipStream_t)stream));
+}
+
+hclrmix_status hclrmix_page_map(const int32_t* cached, const int32_t* fresh, const int32_t* free_pages,
+                                const int32_t* free_start, int32_t* table, int32_t* starts, int32_t* lengths,
+                                int32_t* positions, int32_t* slots, int32_t* taken,
+                                const hclrmix_map_problem* problem, void* stream) {
+  if (!problem) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem must not be NULL");
+  const hclrmix_map_problem& p = *problem;
+  if (p.reserved) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem.reserved must be 0");
+  if (p.batch < 0 || p.tokens < 0 || p.most_pages < 0 || p.free_count < 0 || p.table_stride < 0 || p.page_size < 1)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "sizes must be >= 0, page_size >= 1");
+  if (p.table_stride && p.table_stride < p.most_pages)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "table_stride is shorter than a row of the table");
+  if (p.batch > HCLRMIX_ATTENTION_MAX_BATCH || p.tokens > HCLRMIX_MAX_ROWS || p.page_size > HCLRMIX_MAX_PAGE_SIZE ||
+      p.most_pages > INT32_MAX || p.free_count > INT32_MAX || p.table_stride > MAX_SPAN)
+    return fail(HCLRMIX_ERR_UNSUPPORTED, "at most %d requests, %d tokens and pages of %d rows", HCLRMIX_ATTENTION_MAX_BATCH,
+                HCLRMIX_MAX_ROWS, HCLRMIX_MAX_PAGE_SIZE);
+  if (!starts || !taken || (p.batch > 0 && (!cached || !fresh || !lengths || (p.most_pages > 0 && !table))) ||
+      (p.tokens > 0 && (!positions || !slots)) || (p.free_count > 0 && !free_pages))
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+  struct {
+    const char* name;
+    const void* p;
+  } ints[] = {{"cached", cached}, {"fresh", fresh}, {"free_pages", free_pages}, {"free_start", free_start}, {"table", table},
+              {"starts", starts}, {"lengths", lengths}, {"positions", positions}, {"slots", slots}, {"taken", taken}};
+  for (const auto& i : ints)
+    if (hclrmix_status st = check_ints(i.name, i.p)) return st;
+  hc::MapArgs a{};
+  a.table_stride = p.table_stride ? p.table_stride : p.most_pages;
+  const size_t b4 = 4 * (size_t)p.batch, t4 = 4 * (size_t)p.tokens;
+  const View vc = range("cached", cached, b4, false), vn = range("fresh", fresh, b4, false),
+             vf = range("free_pages", free_pages, 4 * (size_t)p.free_count, false), vi = range("free_start", free_start, 4, false),
+             vt = range("table", table, p.batch && p.most_pages ? 4 * (size_t)((p.batch - 1) * a.table_stride + p.most_pages) : 0, true),
+             vs = range("starts", starts, b4 + 4, true), vl = range("lengths", lengths, b4, true),
+             vp = range("positions", positions, t4, true), vo = range("slots", slots, t4, true),
+             vk = range("taken", taken, b4 + 4, true);
+  if (hclrmix_status st = check_apart({&vc, &vn, &vf, &vi, &vt, &vs, &vl, &vp, &vo, &vk})) return st;
+  a.cached = cached;
+  a.fresh = fresh;
+  a.free_pages = free_pages;
+  a.free_start = free_start;
+  a.table = table;
+  a.tokens = p.tokens;
+  a.free_count = p.free_count;
+  a.batch = (int)p.batch;
+  a.most_pages = (int)p.most_pages;
+  a.page = (int)p.page_size;
+  a.starts = starts;
+  a.lengths = lengths;
+  a.positions = positions;
+  a.slots = slots;
+  a.taken = taken;
+  (void)hipGetLastError();
+  return done(hc::launch_page_map(a, (hipStream_t)stream));
+}
+
+}  // extern "C"

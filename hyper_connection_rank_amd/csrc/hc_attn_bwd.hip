@@ -1,0 +1,506 @@
+// Gradients of attention over whole sequences: hclrmix_attention_backward.
+//
+// With P = exp(s - lse) recomputed from the saved logarithms of the sums, dP = dO V^T, delta = sum over the head's
+// elements of o do, and dS = P (dP - delta):
+//   dq = scale dS K,   dk = scale dS^T Q,   dv = P^T dO,
+// the last two summed over the query heads that share a key head.
+//
+// Two kernels, so that every sum has one owner and a fixed order: k_attention_dq runs over the keys for a tile of
+// query rows (three products), k_attention_dkv over the query rows for a tile of keys (four). Seven products where five
+// would do; adding dq from the second kernel's tiles would need atomics, whose order changes results, or
+// partial sums of q's size for every tile of keys.
+//
+// As in the forward kernel, the block whose registers feed the next product has that product's contraction index in
+// its registers: dq takes S^T (keys in registers, a query per lane), dkv takes S (queries in registers, a key
+// per lane).
+#include "hc_attn.h"
+#include "hc_internal.h"
+
+#include <algorithm>
+
+namespace hc {
+
+// Values on their way into a 16-bit product. fp16 has too few small numbers for dS, whose size is that of the
+// weights (one over the number of keys) times the gradient's: a lane's column is kept scaled by a power of two (exact), chosen
+// from the largest value so far as the running maximum of a softmax is, and the sums with it.
+template <DT D> struct ColumnScale {
+  float by = 0x1p60f;
+  // Brings |x| below 2^15 in this lane's column; sums of it are scaled along.
+  template <int N> __device__ __forceinline__ void apply(f32x16& x, f32x16 (&sums)[N]) {
+    if constexpr (D == DT::F16) {
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+      top = halves_max(top);
+      if (__ballot(top * by > 0x1p15f)) {
+        // top in [2^11, 2^12) of the new scale; infinite values keep the old one
+        const float to = top * by > 0x1p15f && top < __builtin_inff() ? ldexpf(1.0f, 12 - __builtin_amdgcn_frexp_expf(top)) : by;
+        const float f = to / by;
+        by = to;
+#pragma unroll
+        for (int d = 0; d < N; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sums[d][e] *= f;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] *= by;
+    }
+  }
+  __device__ __forceinline__ float undo() const { return D == DT::F16 ? 1.0f / by : 1.0f; }
+};
+
+__device__ __forceinline__ void clear(f32x16& x) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+}
+
+// ------------------------------------------------------------------ dq
+
+template <DT D, int NB> struct DqShape {
+  typedef Rows<D, NB> T;
+  static constexpr int KT = T::RB >= 512 ? 32 : 64, WAVES = 4, TR = 32 * WAVES;
+};
+
+template <DT D, int NB, bool ALN>
+__global__ __launch_bounds__(256, 1) void k_attention_dq(const AttnArgs a) {
+  typedef DqShape<D, NB> F;
+  typedef Rows<D, NB> T;
+  typedef typename T::piece piece;
+  constexpr int KT = F::KT, KB = KT / 32, THREADS = 64 * F::WAVES;
+  constexpr int STEPS = 32 * NB / T::STEP, PSTEPS = 32 / T::STEP;
+  typedef Stager<D, NB, KT, THREADS, ALN> S;
+  constexpr int LDS = 4 * S::BYTES > F::WAVES * 32 * T::RB ? 4 * S::BYTES : F::WAVES * 32 * T::RB;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[LDS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+
+  const int kvh = blockIdx.x % a.kv_heads;
+  const int64_t t = (int64_t)(gridDim.x / a.kv_heads) - 1 - blockIdx.x / a.kv_heads;
+  const Seq s = find_sequence(a, a.q_starts, a.q_tokens, a.group, F::TR, t);
+  const int rows = s.ql * a.group, r0 = s.tile * F::TR;
+  if (s.tile < 0 || r0 >= rows) return;
+  auto base_of = [&](const Strides3& st, bool keys, int head) {
+    return (keys ? (a.k_starts ? s.k0 * st.t : s.b * st.b) : (a.q_starts ? s.q0 * st.t : s.b * st.b)) + head * st.h;
+  };
+  const int h0 = kvh * a.group;
+  const char* kp = (const char*)a.k + base_of(a.sk, true, kvh) * T::ES;
+  const char* vp = (const char*)a.v + base_of(a.sv, true, kvh) * T::ES;
+  const int off = s.kl - s.ql;
+
+  const int mine = r0 + wave * 32 + (lane & 31), r = min(mine, rows - 1), tok = r / a.group, g = r - tok * a.group;
+  piece q[STEPS], go[STEPS];
+  float delta = 0.0f;
+  {
+    const char* pq = (const char*)a.q + (base_of(a.sq, false, h0 + g) + tok * a.sq.t) * T::ES;
+    const char* pg = (const char*)a.d_out + (base_of(a.sdo, false, h0 + g) + tok * a.sdo.t) * T::ES;
+    const char* po = (const char*)a.out + (base_of(a.so, false, h0 + g) + tok * a.so.t) * T::ES;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int col = (2 * i + h) * T::EPC;
+      q[i] = __builtin_bit_cast(piece, chunk16<D, ALN>(pq, col, a.dim));
+      const uint4 w = chunk16<D, ALN>(pg, col, a.dim), y = chunk16<D, ALN>(po, col, a.dim);
+      go[i] = __builtin_bit_cast(piece, w);
+      if constexpr (D == DT::F32) {
+        const f32x4 u = __builtin_bit_cast(f32x4, w), v = __builtin_bit_cast(f32x4, y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) delta = fmaf(u[e], v[e], delta);
+      } else {
+        float u[8], v[8];
+        unpack8<D>(w, u);
+        unpack8<D>(y, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = fmaf(u[e], v[e], delta);
+      }
+    }
+  }
+  delta = halves_sum(delta);
+  const int64_t stat = ((a.q_starts ? s.q0 : s.b * a.q_tokens) + tok) * a.heads + h0 + g;
+  if (lane < 32 && mine < rows) a.delta[stat] = delta;
+  const float lse2 = a.lse[stat] * LOG2E;
+  const Sees see = sees(a, tok + off, s.kl);
+  const Sees wg_first = sees(a, r0 / a.group + off, s.kl);
+  const Sees wg_last = sees(a, min(r0 + F::TR - 1, rows - 1) / a.group + off, s.kl);
+  const KeyTiles tiles = key_tiles<KT>(wg_first, wg_last);
+  const Sees w_first = sees(a, min(r0 + wave * 32, rows - 1) / a.group + off, s.kl);
+  const Sees w_last = sees(a, min(r0 + wave * 32 + 31, rows - 1) / a.group + off, s.kl);
+  const float c = a.scale * LOG2E;
+
+  f32x16 dq[NB];
+#pragma unroll
+  for (int d = 0; d < NB; ++d) clear(dq[d]);
+  ColumnScale<D> scale;
+
+  auto multiply = [&](const unsigned char* kt, const unsigned char* vt, int j0) {
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int i0 = j0 + 32 * k, i1 = i0 + 31;
+      if (i0 > max(w_last.hi, w_last.first - 1) || (i1 < w_first.lo && i0 >= w_last.first)) continue;
+      const bool whole = (i0 >= w_last.lo && i1 <= w_first.hi) || i1 < w_first.first;
+      f32x16 x, y;
+      clear(x);
+      clear(y);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) x = mfma32<D>(T::direct(kt, 32 * k, i, lane), q[i], x);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) y = mfma32<D>(T::direct(vt, 32 * k, i, lane), go[i], y);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], c, -lse2)) * (y[e] - delta);
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = see(i0 + 8 * (e >> 2) + 4 * h + (e & 3)) ? x[e] : 0.0f;
+      }
+      scale.apply(x, dq);
+#pragma unroll
+      for (int i = 0; i < PSTEPS; ++i) {
+        const piece p = piece_of<D>(x, i);
+#pragma unroll
+        for (int d = 0; d < NB; ++d) dq[d] = mfma32<D>(T::transposed(kt, 32 * k + T::STEP * i, d, lane), p, dq[d]);
+      }
+    }
+  };
+
+  const uint32_t ldk = (uint32_t)(a.sk.t * T::ES), ldv = (uint32_t)(a.sv.t * T::ES);
+  auto k_at = [&](int j0) { return kp + (int64_t)j0 * a.sk.t * T::ES; };
+  auto v_at = [&](int j0) { return vp + (int64_t)j0 * a.sv.t * T::ES; };
+  auto k_off = [&](int j) { return (uint32_t)j * ldk; };
+  auto v_off = [&](int j) { return (uint32_t)j * ldv; };
+  if constexpr (ALN) {
+    const uint32_t l0 = lds_offset(lds);
+    auto stage = [&](int i) {
+      const int j0 = tiles(i) * KT, n = s.kl - j0;
+      const uint32_t to = l0 + (i & 1) * 2 * S::BYTES;
+      S::load(k_at(j0), k_off, n, a.dim, to, tid);
+      S::load(v_at(j0), v_off, n, a.dim, to + S::BYTES, tid);
+    };
+    if (tiles.count > 0) stage(0);
+    for (int i = 0; i < tiles.count; ++i) {
+      wait_loads<0>();
+      lds_barrier();
+      if (i + 1 < tiles.count) stage(i + 1);
+      const unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
+      multiply(cur, cur + S::BYTES, tiles(i) * KT);
+    }
+  } else {
+    uint4 fk[S::NL], fv[S::NL];
+    auto fetch = [&](int i) {
+      const int j0 = tiles(i) * KT, n = s.kl - j0;
+      S::fetch(k_at(j0), k_off, n, a.dim, tid, fk);
+      S::fetch(v_at(j0), v_off, n, a.dim, tid, fv);
+    };
+    if (tiles.count > 0) fetch(0);
+    for (int i = 0; i < tiles.count; ++i) {
+      unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
+      S::put(cur, tid, fk);
+      S::put(cur + S::BYTES, tid, fv);
+      lds_barrier();
+      if (i + 1 < tiles.count) fetch(i + 1);
+      multiply(cur, cur + S::BYTES, tiles(i) * KT);
+    }
+  }
+  if (!a.dq) return;
+  lds_barrier();
+  unsigned char* const rows32 = lds + wave * 32 * T::RB;
+  rows_to_lds<D, NB>(rows32, dq, a.scale * scale.undo(), lane);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 4
+  for (int i = lane; i < 32 * T::CPR; i += 64) {
+    const int row = i / T::CPR, rr = r0 + wave * 32 + row, ch = i % T::CPR;
+    if (rr >= rows) continue;
+    const int tk = rr / a.group, hd = rr - tk * a.group;
+    char* to = (char*)a.dq + (base_of(a.sdq, false, h0 + hd) + tk * a.sdq.t) * T::ES;
+    put_chunk16<D, ALN>(to, ch * T::EPC, a.dim, row_chunk<D, NB>(rows32, row, ch));
+  }
+}
+
+// ------------------------------------------------------------------ dk and dv
+
+// NBO: blocks of 32 columns of dk and dv that one workgroup sums (all, or half where the registers hold no more).
+template <DT D, int NB> struct DkvShape {
+  typedef Rows<D, NB> T;
+  static constexpr int QT = T::RB >= 512 ? 32 : 64, WAVES = 4, TK = 32 * WAVES;
+  static constexpr int NBO = NB == 8 ? 4 : NB, HALVES = NB / NBO;
+};
+
+template <DT D, int NB, bool ALN>
+__global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
+  typedef DkvShape<D, NB> F;
+  typedef Rows<D, NB> T;
+  typedef typename T::piece piece;
+  constexpr int QT = F::QT, THREADS = 64 * F::WAVES, NBO = F::NBO;
+  constexpr int STEPS = 32 * NB / T::STEP, PSTEPS = 32 / T::STEP;
+  typedef Stager<D, NB, QT, THREADS, ALN> S;
+  constexpr int GONE = -(1 << 30);  // the position of rows that do not exist
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[4 * S::BYTES];
+  __shared__ __attribute__((aligned(16))) float row_lse[2][QT], row_delta[2][QT];
+  __shared__ __attribute__((aligned(16))) int row_pos[2][QT];
+  static_assert(F::WAVES * 32 * T::RB <= 4 * S::BYTES, "the results fit the staging buffers");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+
+  int id = blockIdx.x;
+  const int d0 = F::HALVES > 1 ? id % F::HALVES * NBO : 0;
+  id /= F::HALVES;
+  const int kvh = id % a.kv_heads;
+  const Seq s = find_sequence(a, a.k_starts, a.k_tokens, 1, F::TK, id / a.kv_heads);
+  const int j0 = s.tile * F::TK;
+  if (s.tile < 0 || j0 >= s.kl) return;
+  auto base_of = [&](const Strides3& st, bool keys, int head) {
+    return (keys ? (a.k_starts ? s.k0 * st.t : s.b * st.b) : (a.q_starts ? s.q0 * st.t : s.b * st.b)) + head * st.h;
+  };
+  const int h0 = kvh * a.group, off = s.kl - s.ql;
+  const int jw = j0 + wave * 32, j = jw + (lane & 31);  // the wave's first key and this lane's
+
+  // The rows that see any of these keys: positions p_lo .. p_hi.
+  const int j_last = min(j0 + F::TK, s.kl) - 1;
+  int p_lo = off, p_hi = s.kl - 1;
+  if (a.causal) p_lo = max(p_lo, j0);
+  if (a.window && j0 >= a.sinks) {
+    p_hi = min(p_hi, j_last + a.window - 1);
+    if (!a.causal) p_lo = max(p_lo, j0 - a.window + 1);
+  }
+  const int r_begin = (p_lo - off) * a.group, r_end = p_hi < p_lo ? r_begin : (p_hi - off + 1) * a.group;
+  const int count = (r_end - r_begin + QT - 1) / QT;
+
+  piece kf[STEPS], vf[STEPS];
+  {
+    const int jc = min(j, s.kl - 1);
+    const char* pk = (const char*)a.k + (base_of(a.sk, true, kvh) + jc * a.sk.t) * T::ES;
+    const char* pv = (const char*)a.v + (base_of(a.sv, true, kvh) + jc * a.sv.t) * T::ES;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      kf[i] = __builtin_bit_cast(piece, chunk16<D, ALN>(pk, (2 * i + h) * T::EPC, a.dim));
+      vf[i] = __builtin_bit_cast(piece, chunk16<D, ALN>(pv, (2 * i + h) * T::EPC, a.dim));
+    }
+  }
+  f32x16 dk[NBO], dv[NBO];
+#pragma unroll
+  for (int d = 0; d < NBO; ++d) {
+    clear(dk[d]);
+    clear(dv[d]);
+  }
+  ColumnScale<D> scale;
+  const float c = a.scale * LOG2E;
+  constexpr float UP = D == DT::F16 ? 15.0f : 0.0f;  // fp16 weights 2^15 times as large, at most 2^15
+
+  auto multiply = [&](const unsigned char* qt, const unsigned char* gt, int buf, int r0) {
+#pragma unroll
+    for (int b = 0; b < QT / 32; ++b) {
+      const int ra = r0 + 32 * b, rz = min(ra + 32, r_end) - 1;
+      if (ra >= r_end) continue;
+      const int pa = ra / a.group + off, pz = rz / a.group + off;  // the block's first and last positions
+      const int jz = jw + 31;
+      if (a.causal && pz < jw) continue;
+      if (a.window && jw >= a.sinks && (jz <= pa - a.window || (!a.causal && jw >= pz + a.window))) continue;
+      if (jw >= s.kl) continue;
+      const bool whole = ra + 32 <= r_end && jz < s.kl && (!a.causal || jz <= pa) &&
+                         (!a.window || (jw > pz - a.window && (a.causal || jz < pa + a.window)) || jz < a.sinks);
+      f32x16 x, y;
+      clear(x);
+      clear(y);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) x = mfma32<D>(T::direct(qt, 32 * b, i, lane), kf[i], x);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) y = mfma32<D>(T::direct(gt, 32 * b, i, lane), vf[i], y);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const f32x4 nl = *(const f32x4*)&row_lse[buf][32 * b + 8 * u + 4 * h];
+        const f32x4 dl = *(const f32x4*)&row_delta[buf][32 * b + 8 * u + 4 * h];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(x[4 * u + e], c, UP - nl[e]));
+          x[4 * u + e] = p;
+          y[4 * u + e] = p * (y[4 * u + e] - dl[e]) * (D == DT::F16 ? 0x1p-15f : 1.0f);
+        }
+      }
+      if (!whole) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int4 pos = *(const int4*)&row_pos[buf][32 * b + 8 * u + 4 * h];
+          const int pp[4] = {pos.x, pos.y, pos.z, pos.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int p = pp[e], far = p - j;
+            const bool in = p > GONE && j < s.kl && (!a.causal || far >= 0) &&
+                            (!a.window || (far < a.window && far > -a.window) || j < a.sinks);
+            x[4 * u + e] = in ? x[4 * u + e] : 0.0f;
+            y[4 * u + e] = in ? y[4 * u + e] : 0.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PSTEPS; ++i) {
+        const piece p = piece_of<D>(x, i);
+#pragma unroll
+        for (int d = 0; d < NBO; ++d) dv[d] = mfma32<D>(T::transposed(gt, 32 * b + T::STEP * i, d0 + d, lane), p, dv[d]);
+      }
+      scale.apply(y, dk);
+#pragma unroll
+      for (int i = 0; i < PSTEPS; ++i) {
+        const piece p = piece_of<D>(y, i);
+#pragma unroll
+        for (int d = 0; d < NBO; ++d) dk[d] = mfma32<D>(T::transposed(qt, 32 * b + T::STEP * i, d0 + d, lane), p, dk[d]);
+      }
+    }
+  };
+
+  // This thread's rows of the tile being loaded: query and head of each, QT rows further with every tile.
+  const int step_t = QT / a.group, step_g = QT - step_t * a.group;
+  int tk[S::NL], hd[S::NL], st_t, st_g;
+#pragma unroll
+  for (int i = 0; i < S::NL; ++i) {
+    const int r = r_begin + S::row(i, tid);
+    tk[i] = r / a.group;
+    hd[i] = r - tk[i] * a.group;
+  }
+  st_t = (r_begin + (tid & (QT - 1))) / a.group;
+  st_g = r_begin + (tid & (QT - 1)) - st_t * a.group;
+  auto advance = [&](int& tok, int& g) {
+    tok += step_t;
+    g += step_g;
+    if (g >= a.group) {
+      g -= a.group;
+      ++tok;
+    }
+  };
+  const int t_end = p_hi - off + 1;  // queries before this one
+  const char* qp = (const char*)a.q + base_of(a.sq, false, h0) * T::ES;
+  const char* gp = (const char*)a.d_out + base_of(a.sdo, false, h0) * T::ES;
+  const int64_t stat0 = (a.q_starts ? s.q0 : s.b * a.q_tokens) * a.heads + h0;
+  float n_lse = 0.0f, n_delta = 0.0f;
+  int n_pos = GONE;
+  auto fetch_stats = [&]() {  // of the next tile, into registers
+    const bool in = st_t < t_end;
+    const int64_t at = stat0 + (int64_t)(in ? st_t : 0) * a.heads + st_g;
+    n_lse = in ? a.lse[at] * LOG2E : 0.0f;
+    n_delta = in ? a.delta[at] : 0.0f;
+    n_pos = in ? st_t + off : GONE;
+    advance(st_t, st_g);
+  };
+  auto put_stats = [&](int buf) {
+    if (tid < QT) {
+      row_lse[buf][tid] = n_lse;
+      row_delta[buf][tid] = n_delta;
+      row_pos[buf][tid] = n_pos;
+    }
+  };
+  if constexpr (ALN) {
+    const uint32_t l0 = lds_offset(lds);
+    auto stage = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < S::NL; ++i) {
+        const int col = S::col(i, tid);
+        const bool in = tk[i] < t_end && col < a.dim;
+        const char* pq = in ? qp + (tk[i] * a.sq.t + hd[i] * a.sq.h + col) * T::ES : (const char*)zeros16;
+        const char* pg = in ? gp + (tk[i] * a.sdo.t + hd[i] * a.sdo.h + col) * T::ES : (const char*)zeros16;
+        const uint32_t to = __builtin_amdgcn_readfirstlane(l0 + buf * 2 * S::BYTES + (i * THREADS + wave * 64) * 16);
+        lds_load_from(pq, to);
+        lds_load_from(pg, to + S::BYTES);
+        advance(tk[i], hd[i]);
+      }
+    };
+    if (count > 0) {
+      fetch_stats();
+      put_stats(0);
+      if (count > 1) fetch_stats();
+      stage(0);
+    }
+    for (int i = 0; i < count; ++i) {
+      // Tile i and the next tile's statistics have arrived; every wave is done with tile i - 1.
+      wait_loads<0>();
+      lds_barrier();
+      if (i + 1 < count) {
+        put_stats((i + 1) & 1);
+        fetch_stats();
+        stage((i + 1) & 1);
+      }
+      const unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
+      multiply(cur, cur + S::BYTES, i & 1, r_begin + i * QT);
+    }
+  } else {
+    uint4 fq[S::NL], fg[S::NL];
+    auto fetch = [&]() {
+      fetch_stats();
+#pragma unroll
+      for (int i = 0; i < S::NL; ++i) {
+        fq[i] = fg[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (tk[i] < t_end) {
+          fq[i] = chunk16<D, false>(qp + (tk[i] * a.sq.t + hd[i] * a.sq.h) * T::ES, S::col(i, tid), a.dim);
+          fg[i] = chunk16<D, false>(gp + (tk[i] * a.sdo.t + hd[i] * a.sdo.h) * T::ES, S::col(i, tid), a.dim);
+        }
+        advance(tk[i], hd[i]);
+      }
+    };
+    if (count > 0) fetch();
+    for (int i = 0; i < count; ++i) {
+      unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
+      S::put(cur, tid, fq);
+      S::put(cur + S::BYTES, tid, fg);
+      put_stats(i & 1);
+      lds_barrier();
+      if (i + 1 < count) fetch();
+      multiply(cur, cur + S::BYTES, i & 1, r_begin + i * QT);
+    }
+  }
+  lds_barrier();
+
+  unsigned char* const rows32 = lds + wave * 32 * T::RB;
+  auto write = [&](void* base, const Strides3& st, const f32x16 (&sum)[NBO], float f) {
+    if (!base) return;
+    rows_to_lds<D, NB>(rows32, sum, f, lane);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    constexpr int CPR = 32 * NBO / T::EPC;
+#pragma unroll 4
+    for (int i = lane; i < 32 * CPR; i += 64) {
+      const int row = i / CPR, ch = i % CPR;
+      if (jw + row >= s.kl) continue;
+      char* to = (char*)base + (base_of(st, true, kvh) + (jw + row) * st.t) * T::ES;
+      put_chunk16<D, ALN>(to, 32 * d0 + ch * T::EPC, a.dim, row_chunk<D, NB>(rows32, row, ch));
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+  write(a.dv, a.sdv, dv, D == DT::F16 ? 0x1p-15f : 1.0f);
+  write(a.dk, a.sdk, dk, a.scale * scale.undo());
+}
+
+namespace {
+
+template <DT D, int NB> hipError_t go(const AttnArgs& a0, bool aligned, hipStream_t s) {
+  AttnArgs a = a0;
+  auto tiles = [&](const int* starts, int64_t units, int tr) {
+    a.tiles = (int)((units + tr - 1) / tr);
+    return starts ? units / tr + a.batch : (int64_t)a.tiles * a.batch;
+  };
+  if (a.q_tokens > 0) {
+    const int64_t n = tiles(a.q_starts, a.q_tokens * a.group, DqShape<D, NB>::TR);
+    const dim3 grid((unsigned)(n * a.kv_heads)), block(64 * DqShape<D, NB>::WAVES);
+    if (aligned) hipLaunchKernelGGL((k_attention_dq<D, NB, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_attention_dq<D, NB, false>), grid, block, 0, s, a);
+  }
+  if ((a.dk || a.dv) && a.k_tokens > 0) {
+    const int64_t n = tiles(a.k_starts, a.k_tokens, DkvShape<D, NB>::TK);
+    const dim3 grid((unsigned)(n * a.kv_heads * DkvShape<D, NB>::HALVES)), block(64 * DkvShape<D, NB>::WAVES);
+    if (aligned) hipLaunchKernelGGL((k_attention_dkv<D, NB, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_attention_dkv<D, NB, false>), grid, block, 0, s, a);
+  }
+  return hipGetLastError();
+}
+template <DT D> hipError_t go_dim(const AttnArgs& a, bool aligned, hipStream_t s) {
+  if (a.dim <= 64) return go<D, 2>(a, aligned, s);
+  if (a.dim <= 96) return go<D, 3>(a, aligned, s);
+  if (a.dim <= 128) return go<D, 4>(a, aligned, s);
+  return go<D, 8>(a, aligned, s);
+}
+
+}  // namespace
+
+hipError_t launch_attention_backward(AttnArgs a, int dtype, bool aligned, hipStream_t s) {
+  switch (dtype) {
+    case (int)DT::F32: return go_dim<DT::F32>(a, aligned, s);
+    case (int)DT::F16: return go_dim<DT::F16>(a, aligned, s);
+    default: return go_dim<DT::BF16>(a, aligned, s);
+  }
+}
+
+size_t attention_backward_scratch(const AttnArgs& a, int) {
+  return (size_t)(a.q_starts ? a.q_tokens : a.batch * a.q_tokens) * a.heads * sizeof(float);
+}
+
+}  // namespace hc

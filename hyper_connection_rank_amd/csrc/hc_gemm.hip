@@ -23,6 +23,7 @@
 #include "hc_ffn.h"
 #include "hc_internal.h"
 #include "hc_plan.h"
+#include "hc_stage.h"
 
 #include "../../include/hclrmix.h"
 
@@ -224,7 +225,6 @@ __device__ __forceinline__ void finish_rows(const Gemm& a, int b, const float* s
   }
 }
 
-constexpr uint32_t OUTSIDE = 0x80000000u;  // an offset past every descriptor's end: loads give zeros, stores nothing
 constexpr int AGENT = 16;  // sc1: the access is coherent across the chip's L2s
 
 // Split sums: this workgroup's tile goes to scratch; the last of the tile's workgroups to
@@ -325,35 +325,6 @@ __device__ __forceinline__ Place place(const Gemm& a) {
 // so the chunk permutation is applied to the addresses instead. Loads go
 // through a buffer descriptor of the tile; lanes whose chunk lies outside the
 // operand get an offset beyond it, for which the load writes zeros.
-__device__ __forceinline__ u32x4 raw_desc(const void* base) {
-  const uint64_t b = (uint64_t)base;
-  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
-               (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)), 0x7FFFFFF0u, 0x00020000u};
-}
-__device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(const lds_u8*)p; }
-// Lane l: W bytes (16 or 4) from offset off of the descriptor to LDS byte dst + W l (dst
-// the same in every lane). Written out because the compiler, which cannot tell the stage
-// being filled from the one being read, would wait for the load before every LDS read. m0 is a
-// register of the compiler's own (it warns of any asm that writes it): named as written, so that
-// no value that the compiler put there itself is taken to have survived.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-template <int W, bool STREAM> __device__ __forceinline__ void lds_load(u32x4 desc, uint32_t off, uint32_t dst) {
-  static_assert(W == 16 || W == 4, "width");
-  if constexpr (W == 4 && STREAM)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen nt lds"
-                 : : "s"(dst), "v"(off), "s"(desc) : "memory", "m0");
-  else if constexpr (W == 4)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 : : "s"(dst), "v"(off), "s"(desc) : "memory", "m0");
-  else if constexpr (STREAM)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
-                 : : "s"(dst), "v"(off), "s"(desc) : "memory", "m0");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 : : "s"(dst), "v"(off), "s"(desc) : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 // Where an operand's next tile starts and how many contraction indices it has from
 // there in its segment; steps go through the first segment, then the second.
@@ -431,18 +402,6 @@ template <DT D, bool TR, int R, int THREADS, int W> struct Direct {
     }
   }
 };
-
-// Waits until at most N of this wave's loads are in flight (they complete in order).
-template <int N> __device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
-}
-
-// Workgroup barrier once this wave's LDS operations are done; its global loads stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 // BM x BN tile, WM x WN waves, contraction steps of 128 bytes staged in a ring of NST buffers: the
 // loads of step t + NST - 1 are issued once every wave is done with step t - 1, whose buffer

@@ -462,6 +462,171 @@ hclrmix_status hclrmix_linear_backward_workspace_size(const hclrmix_product* pro
 hclrmix_status hclrmix_glu_workspace_size(const hclrmix_product* problem, size_t* bytes);
 hclrmix_status hclrmix_glu_backward_workspace_size(const hclrmix_product* problem, size_t* bytes);
 
+/* ------------------------------------------------------------------------
+ * Attention between two blocks: over whole sequences with its gradients, and
+ * for one new token of each sequence over a key-value cache in pages, with
+ * what writes that cache. The rules of the operators above hold here too
+ * (element type T, fp32 sums and softmax statistics, one rounding of each
+ * output, fixed orders, host checks, nothing allocated), with what is said
+ * below.
+ *
+ * There are `heads` query heads and `kv_heads` key heads, the former a
+ * multiple of the latter: query head h reads key head h / (heads / kv_heads).
+ * A sequence has q_len queries and k_len keys; query i stands at position
+ * p = i + k_len - q_len (the last query at the last key). It sees key j if
+ *   (not causal or j <= p) and (window == 0 or |p - j| < window or j < sinks):
+ * a window of `window` keys up to its own, and the sequence's first `sinks`
+ * keys, which stay visible. Of the keys that it sees,
+ *   s_j = scale * q.k_j,  lse = log sum_j exp(s_j),  out = sum_j exp(s_j - lse) v_j;
+ * a query that sees none has out = 0 and lse = -infinity.
+ *
+ *  - 16-bit products: the weights exp(s_j - m) (and in the backward pass
+ *    those and dS) are rounded to T as the matrix units' operands, with m
+ *    within 8 powers of two of the largest score. Sums of the weights take
+ *    them before that rounding.
+ *  - Values of keys that a query does not see do not reach its results,
+ *    except that infinities and NaN in v (backward: in q, k, v or d_out)
+ *    may: a weight of zero times an infinity is NaN. Rows that belong to no
+ *    sequence, and rows of pages behind a sequence's last key or outside its
+ *    window, may hold anything.
+ *  - Contents of starts, tables, lengths and slots are not checked on the
+ *    host. Kernels hold them inside the tensors: no access leaves them, but
+ *    results of wrong contents are unspecified, unless said otherwise. */
+
+#define HCLRMIX_ATTENTION_MAX_HEADS 1024
+#define HCLRMIX_ATTENTION_MAX_DIM 256
+#define HCLRMIX_ATTENTION_MAX_BATCH 65536
+#define HCLRMIX_MAX_PAGE_SIZE 65536
+
+/* Strides in elements of a tensor [sequence][token][head][dim] (a cache:
+ * [page][row][head][dim]); dim is contiguous. A 0 counts as contiguous:
+ * head dim, token heads * head, sequence tokens * token. Any order of the
+ * three is allowed as long as no two rows overlap. token is at most 2^21,
+ * the others at most 2^40. */
+typedef struct {
+  int64_t sequence, token, head;
+} hclrmix_strides;
+
+typedef struct {
+  int64_t batch;     /* sequences, 0 to HCLRMIX_ATTENTION_MAX_BATCH */
+  int64_t q_tokens;  /* queries of each sequence; packed: rows of q */
+  int64_t k_tokens;  /* keys of each sequence; packed: rows of k and v */
+  int32_t heads, kv_heads;
+  int32_t dim;       /* of a head, 1 to HCLRMIX_ATTENTION_MAX_DIM */
+  int32_t dtype;     /* hclrmix_dtype */
+  int32_t causal;    /* 0 or 1 */
+  int32_t window;    /* 0: none */
+  int32_t sinks;     /* first keys outside the window that stay visible; without a window of no effect */
+  int32_t packed;    /* 1: sequences lie one after another, at starts */
+  float scale;       /* > 0 */
+  int32_t reserved[2];                  /* must be 0 */
+  hclrmix_strides q, k, v, out;         /* .sequence is not used of packed tensors */
+  hclrmix_strides d_out, dq, dk, dv;    /* backward only */
+} hclrmix_attention_problem;
+
+/* out [.., q_tokens, heads, dim] from q (the same shape) and k, v
+ * [.., k_tokens, kv_heads, dim]. lse, fp32 [.., q_tokens, heads] contiguous
+ * or NULL, receives the logarithms that the backward pass takes.
+ * Packed: q_starts [batch + 1] int32 device memory, ascending: sequence b's
+ * queries are rows q_starts[b] to q_starts[b + 1] - 1; k_starts likewise for
+ * keys, or NULL where they are the same. Rows outside every sequence are
+ * neither read nor written. Not packed: both NULL.
+ * rows and heads: tokens of all sequences times heads at most 2^29, batch
+ * times heads at most 2^20. */
+hclrmix_status hclrmix_attention(const void* q, const void* k, const void* v, const int32_t* q_starts,
+                                 const int32_t* k_starts, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, const hclrmix_attention_problem* problem, void* stream);
+
+/* Gradients of hclrmix_attention from its inputs, its out and lse, and
+ * d_out: with P = exp(s - lse) and dS = P (d_out.v - sum_dim out d_out),
+ *   dq = scale dS k,  dk = scale dS^T q,  dv = P^T d_out,
+ * dk and dv summed over the query heads of a key head. Each of dq, dk, dv may
+ * be NULL when not wanted, at least one wanted. dq, dk and dv may be columns
+ * of the rows of one tensor, as q, k and v may. */
+hclrmix_status hclrmix_attention_backward(const void* q, const void* k, const void* v, const void* out,
+                                          const float* lse, const void* d_out, const int32_t* q_starts,
+                                          const int32_t* k_starts, void* dq, void* dk, void* dv, void* workspace,
+                                          size_t workspace_bytes, const hclrmix_attention_problem* problem,
+                                          void* stream);
+
+/* Workspace of each, for any strides and masks, with these batch and tokens
+ * or fewer. */
+hclrmix_status hclrmix_attention_workspace_size(const hclrmix_attention_problem* problem, size_t* bytes);
+hclrmix_status hclrmix_attention_backward_workspace_size(const hclrmix_attention_problem* problem, size_t* bytes);
+
+typedef struct {
+  int64_t batch;         /* sequences */
+  int64_t pages;         /* of each cache */
+  int64_t page_size;     /* rows of a page, 1 to HCLRMIX_MAX_PAGE_SIZE */
+  int64_t most_pages;    /* entries of a sequence's row in the table; times page_size at most 2^29 */
+  int64_t table_stride;  /* entries from one row of the table to the next (0: most_pages) */
+  int32_t heads, kv_heads, dim, dtype;
+  int32_t window, sinks;
+  float scale;
+  int32_t reserved;      /* must be 0 */
+  hclrmix_strides q, out;  /* [sequence][head][dim]; .token is not used */
+  hclrmix_strides cache;   /* of both caches: .sequence from page to page, .token from row to row */
+} hclrmix_paged_problem;
+
+/* Attention of one new token of each sequence (causal, at position
+ * lengths[b] - 1, its key and value in the cache already): out
+ * [batch, heads, dim] from q and the caches [pages, page_size, kv_heads, dim].
+ * Key j of sequence b is row j % page_size of page table[b][j / page_size].
+ * Keys on pages that the cache does not have (negative, or >= pages) count as
+ * not seen; a length is held to 0 .. most_pages * page_size. Pages outside
+ * the window (beyond the first `sinks` keys) are not read. */
+hclrmix_status hclrmix_paged_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* table,
+                                       const int32_t* lengths, void* out, void* workspace, size_t workspace_bytes,
+                                       const hclrmix_paged_problem* problem, void* stream);
+
+/* Enough for these batch and most_pages or fewer. */
+hclrmix_status hclrmix_paged_attention_workspace_size(const hclrmix_paged_problem* problem, size_t* bytes);
+
+typedef struct {
+  int64_t tokens, pages, page_size;
+  int32_t kv_heads, dim, dtype, reserved;  /* reserved must be 0 */
+  hclrmix_strides k, v;   /* [token][head][dim]; .sequence is not used */
+  hclrmix_strides cache;  /* of both caches, as above */
+} hclrmix_store_problem;
+
+/* Row t of k and v [tokens, kv_heads, dim] into row slots[t] % page_size of
+ * page slots[t] / page_size. Rows whose slot is negative, or outside the
+ * cache, go nowhere. Slots that occur once are stored whole; of rows that
+ * name the same slot, it is left open which one each element is from. */
+hclrmix_status hclrmix_cache_store(const void* k, const void* v, const int32_t* slots, void* k_cache, void* v_cache,
+                                   const hclrmix_store_problem* problem, void* stream);
+
+typedef struct {
+  int64_t batch;         /* requests */
+  int64_t tokens;        /* rows of the batch's new tokens, padding included */
+  int64_t page_size;
+  int64_t most_pages;    /* entries of a request's row in the table */
+  int64_t table_stride;  /* 0: most_pages */
+  int64_t free_count;    /* entries of free_pages */
+  int32_t reserved;      /* must be 0 */
+} hclrmix_map_problem;
+
+/* Tables of a step that brings fresh[b] new tokens to request b, which has
+ * cached[b] in the cache (all arrays int32 device memory; negative counts are
+ * taken as 0):
+ *   starts [batch + 1]  sums of fresh before each request, and of all
+ *   taken [batch + 1]   pages that the requests before each one, and all, lack
+ *   lengths [batch]     cached + fresh
+ *   table [batch, most_pages], in place: the pages that request b lacks,
+ *     entries from ceil(cached / page_size) on, are free_pages[first + taken[b]]
+ *     and the following, with first = *free_start (NULL: 0); -1 where
+ *     free_pages has ended. Other entries stay as they were.
+ *   positions, slots [tokens]  of row t, token t - starts[b] of its request:
+ *     cached[b] + that, and the row's place in the cache (page * page_size +
+ *     row in the page), or -1 where it has no page. Rows behind the last
+ *     request: 0 and -1, so that hclrmix_cache_store passes over them.
+ * Repeating the call with the same inputs repeats its results. Sums are held
+ * to 2^31 - 1. No two arrays may overlap. */
+hclrmix_status hclrmix_page_map(const int32_t* cached, const int32_t* fresh, const int32_t* free_pages,
+                                const int32_t* free_start, int32_t* table, int32_t* starts, int32_t* lengths,
+                                int32_t* positions, int32_t* slots, int32_t* taken,
+                                const hclrmix_map_problem* problem, void* stream);
+
 /* Static description of a status code. */
 const char* hclrmix_status_string(hclrmix_status status);
 
