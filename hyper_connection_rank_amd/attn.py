@@ -38,7 +38,7 @@ def _strides(*names):
 class AttentionProblem(ctypes.Structure):
     _fields_ = [("batch", _I64), ("q_tokens", _I64), ("k_tokens", _I64), ("heads", _I32), ("kv_heads", _I32), ("dim", _I32),
                 ("dtype", _I32), ("causal", _I32), ("window", _I32), ("sinks", _I32), ("packed", _I32), ("scale", _F32),
-                ("reserved", _I32 * 2)] + _strides("q", "k", "v", "out", "d_out", "dq", "dk", "dv")
+                ("reserved", _I32 * 2)] + _strides("q", "k", "v", "out", "d_out", "dq", "dk", "dv", "lse")
 
 
 class PagedProblem(ctypes.Structure):
@@ -123,8 +123,12 @@ def _rows(t, like, shape, name):
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         _refuse(f"{name}'s last dimension must be contiguous")
+    return _row_strides(shape[:-1], st, name)
+
+
+def _row_strides(shape, strides, name):
     out = []
-    for n, s in zip(shape[:-1], st):
+    for n, s in zip(shape, strides):
         if n > 1 and s == 0:
             _refuse(f"{name} must have rows of its own; expand()ed tensors are refused")
         out.append(s if n > 1 else 0)
@@ -225,8 +229,8 @@ def attention_backward(q, k, v, out, lse, d_out, *, causal=True, window=0, sinks
     allocates."""
     _unrecorded(q, k, v, out, d_out)
     fields, st = _whole(q, k, v, causal, window, sinks, scale, q_starts, k_starts)
-    if lse.dtype is not torch.float32 or lse.device != q.device or lse.shape != q.shape[:-1] or not lse.is_contiguous():
-        _refuse(f"lse must be contiguous float32 {tuple(q.shape[:-1])}")
+    if lse.dtype is not torch.float32 or lse.device != q.device or lse.shape != q.shape[:-1]:
+        _refuse(f"lse must be float32 {tuple(q.shape[:-1])} on the tensors' device")
     st += _rows(out, q, q.shape, "out") + _rows(d_out, q, q.shape, "d_out")
     if grads is None:
         new = torch.empty if q_starts is None else torch.zeros
@@ -234,7 +238,7 @@ def attention_backward(q, k, v, out, lse, d_out, *, causal=True, window=0, sinks
     dq, dk, dv = grads
     for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
         st += (0, 0, 0) if t is None else _rows(t, q, like.shape, name)
-    p = AttentionProblem(*fields, *st)
+    p = AttentionProblem(*fields, *st, *_row_strides(lse.shape, lse.stride(), "lse"))
     if workspace is None:
         need = hclrmix_attention_backward_workspace_size(p)
         workspace = _scratch(None, need, q.device)

@@ -21,9 +21,9 @@ struct Strides3 {
 struct AttnArgs {
   const void *q, *k, *v;
   void* out;                   // forward: written; backward: as saved
-  float* lse;                  // [rows of q][heads], natural logarithm; forward: or null
+  float* lse;                  // [q_tokens][heads] at strides sl, natural logarithm; forward: or null
   const int *q_starts, *k_starts;  // [batch + 1] of packed sequences, or null
-  Strides3 sq, sk, sv, so;
+  Strides3 sq, sk, sv, so, sl;
   int64_t q_tokens, k_tokens;  // of a sequence; packed: of all
   int batch, heads, kv_heads, group, dim;
   int causal, window, sinks;   // window 0: none

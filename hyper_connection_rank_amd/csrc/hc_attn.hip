@@ -204,7 +204,7 @@ __global__ __launch_bounds__(256, 1) void k_attention(const AttnArgs a) {
     const int first = r0 + (wave * QB + b) * 32;
     if (a.lse && lane < 32 && first + row < rows) {
       const int r = first + row, tok = r / a.group;
-      const int64_t at = ((a.q_starts ? s.q0 : s.b * a.q_tokens) + tok) * a.heads + kvh * a.group + r - tok * a.group;
+      const int64_t at = (a.q_starts ? s.q0 * a.sl.t : s.b * a.sl.b) + tok * a.sl.t + (kvh * a.group + r - tok * a.group) * a.sl.h;
       a.lse[at] = total == 0.0f ? NEG_INF : (m[b] - weight_shift<D>() + __builtin_amdgcn_logf(total)) * LN2;
     }
   }

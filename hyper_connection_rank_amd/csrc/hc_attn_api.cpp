@@ -267,7 +267,8 @@ hclrmix_status hclrmix_attention(const void* q, const void* k, const void* v, co
   if (hclrmix_status st = check_starts(p, q_starts, k_starts)) return st;
   const size_t es = elem_size(p.dtype);
   const Extent e = extent(p);
-  View vq, vk, vv, vo;
+  View vq, vk, vv, vo, vl;
+  if (hclrmix_status st = view(vl, "lse", lse, p.lse, e.n, e.q, p.heads, 1, 4, true)) return st;
   if (hclrmix_status st = view(vq, "q", q, p.q, e.n, e.q, p.heads, p.dim, es, false)) return st;
   if (hclrmix_status st = view(vk, "k", k, p.k, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
   if (hclrmix_status st = view(vv, "v", v, p.v, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
@@ -275,10 +276,9 @@ hclrmix_status hclrmix_attention(const void* q, const void* k, const void* v, co
   if (p.batch == 0 || p.q_tokens == 0) return ok();
   if (!q || !out || (p.k_tokens > 0 && (!k || !v)))
     return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "q, k, v and out are required");
-  if ((uintptr_t)lse & 3u) return fail(HCLRMIX_ERR_UNSUPPORTED, "lse must be element-aligned");
   const size_t need = attention_need(problem);
   const View vs = range("q_starts", q_starts, 4 * (p.batch + 1), false), vt = range("k_starts", k_starts, 4 * (p.batch + 1), false),
-             vl = range("lse", lse, 4 * (size_t)(e.n * e.q * p.heads), true), vw = range("workspace", workspace, std::min(need, workspace_bytes), true);
+             vw = range("workspace", workspace, std::min(need, workspace_bytes), true);
   if (hclrmix_status st = check_apart({&vq, &vk, &vv, &vo, &vs, &vt, &vl, &vw})) return st;
   if (hclrmix_status st = check_workspace(workspace, workspace_bytes, need)) return st;
   hc::AttnArgs a = attention_args(problem);
@@ -293,6 +293,7 @@ hclrmix_status hclrmix_attention(const void* q, const void* k, const void* v, co
   a.sk = strides(vk);
   a.sv = strides(vv);
   a.so = strides(vo);
+  a.sl = strides(vl);
   a.partial = (float*)((char*)workspace + HCLRMIX_COUNTER_BYTES);
   (void)hipGetLastError();
   return done(hc::launch_attention(a, p.dtype, aligned16({&vq, &vk, &vv, &vo}), (hipStream_t)stream));
@@ -309,7 +310,8 @@ hclrmix_status hclrmix_attention_backward(const void* q, const void* k, const vo
   if (!dq && !dk && !dv) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "no gradient is wanted");
   const size_t es = elem_size(p.dtype);
   const Extent e = extent(p);
-  View vq, vk, vv, vo, vg, wq, wk, wv;
+  View vq, vk, vv, vo, vg, vl, wq, wk, wv;
+  if (hclrmix_status st = view(vl, "lse", lse, p.lse, e.n, e.q, p.heads, 1, 4, false)) return st;
   if (hclrmix_status st = view(vq, "q", q, p.q, e.n, e.q, p.heads, p.dim, es, false)) return st;
   if (hclrmix_status st = view(vk, "k", k, p.k, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
   if (hclrmix_status st = view(vv, "v", v, p.v, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
@@ -321,10 +323,9 @@ hclrmix_status hclrmix_attention_backward(const void* q, const void* k, const vo
   if (p.batch == 0 || (p.q_tokens == 0 && p.k_tokens == 0)) return ok();
   if ((p.q_tokens > 0 && (!q || !out || !d_out || !lse)) || (p.k_tokens > 0 && (!k || !v)))
     return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "q, k, v, out, lse and d_out are required");
-  if ((uintptr_t)lse & 3u) return fail(HCLRMIX_ERR_UNSUPPORTED, "lse must be element-aligned");
   const size_t need = attention_backward_need(problem);
   const View vs = range("q_starts", q_starts, 4 * (p.batch + 1), false), vt = range("k_starts", k_starts, 4 * (p.batch + 1), false),
-             vl = range("lse", lse, 4 * (size_t)(e.n * e.q * p.heads), false), vw = range("workspace", workspace, std::min(need, workspace_bytes), true);
+             vw = range("workspace", workspace, std::min(need, workspace_bytes), true);
   if (hclrmix_status st = check_apart({&vq, &vk, &vv, &vo, &vg, &wq, &wk, &wv, &vs, &vt, &vl, &vw})) return st;
   if (hclrmix_status st = check_workspace(workspace, workspace_bytes, need)) return st;
   hc::AttnArgs a = attention_args(problem);
@@ -343,6 +344,7 @@ hclrmix_status hclrmix_attention_backward(const void* q, const void* k, const vo
   a.sk = strides(vk);
   a.sv = strides(vv);
   a.so = strides(vo);
+  a.sl = strides(vl);
   a.sdo = strides(vg);
   a.sdq = strides(wq);
   a.sdk = strides(wk);

@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_dq(const AttnArgs a) {
   delta = halves_sum(delta);
   const int64_t stat = ((a.q_starts ? s.q0 : s.b * a.q_tokens) + tok) * a.heads + h0 + g;
   if (lane < 32 && mine < rows) a.delta[stat] = delta;
-  const float lse2 = a.lse[stat] * LOG2E;
+  const float lse2 = a.lse[base_of(a.sl, false, h0 + g) + tok * a.sl.t] * LOG2E;
   const Sees see = sees(a, tok + off, s.kl);
   const Sees wg_first = sees(a, r0 / a.group + off, s.kl);
   const Sees wg_last = sees(a, min(r0 + F::TR - 1, rows - 1) / a.group + off, s.kl);
@@ -364,12 +364,13 @@ __global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
   const char* qp = (const char*)a.q + base_of(a.sq, false, h0) * T::ES;
   const char* gp = (const char*)a.d_out + base_of(a.sdo, false, h0) * T::ES;
   const int64_t stat0 = (a.q_starts ? s.q0 : s.b * a.q_tokens) * a.heads + h0;
+  const int64_t lse0 = base_of(a.sl, false, h0);
   float n_lse = 0.0f, n_delta = 0.0f;
   int n_pos = GONE;
   auto fetch_stats = [&]() {  // of the next tile, into registers
     const bool in = st_t < t_end;
     const int64_t at = stat0 + (int64_t)(in ? st_t : 0) * a.heads + st_g;
-    n_lse = in ? a.lse[at] * LOG2E : 0.0f;
+    n_lse = in ? a.lse[lse0 + st_t * a.sl.t + st_g * a.sl.h] * LOG2E : 0.0f;
     n_delta = in ? a.delta[at] : 0.0f;
     n_pos = in ? st_t + off : GONE;
     advance(st_t, st_g);

@@ -522,11 +522,12 @@ typedef struct {
   int32_t reserved[2];                  /* must be 0 */
   hclrmix_strides q, k, v, out;         /* .sequence is not used of packed tensors */
   hclrmix_strides d_out, dq, dk, dv;    /* backward only */
+  hclrmix_strides lse;                  /* [sequence][token][head], in floats */
 } hclrmix_attention_problem;
 
 /* out [.., q_tokens, heads, dim] from q (the same shape) and k, v
- * [.., k_tokens, kv_heads, dim]. lse, fp32 [.., q_tokens, heads] contiguous
- * or NULL, receives the logarithms that the backward pass takes.
+ * [.., k_tokens, kv_heads, dim]. lse, fp32 [.., q_tokens, heads] or NULL,
+ * receives the logarithms that the backward pass takes.
  * Packed: q_starts [batch + 1] int32 device memory, ascending: sequence b's
  * queries are rows q_starts[b] to q_starts[b + 1] - 1; k_starts likewise for
  * keys, or NULL where they are the same. Rows outside every sequence are

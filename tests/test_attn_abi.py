@@ -79,7 +79,7 @@ COMMON = [("dtype", 11, U), ("heads", 0, E), ("kv_heads", 0, E), ("kv_heads", 3,
 @pytest.mark.parametrize("field,value,status", COMMON + [
     ("causal", 2, E), ("causal", -1, E), ("packed", 2, E), ("q_tokens", -1, E), ("k_tokens", -1, E), ("q_tokens", (1 << 21) + 1, U),
     ("k_tokens", (1 << 21) + 1, U), ("heads", 514, E), ("q_token", (1 << 21) + 1, U), ("k_sequence", (1 << 40) + 1, U), ("q_head", -1, E),
-    ("v_token", -1, E), ("out_sequence", -1, E), ("q_token", 511, E), ("k_head", 63, E), ("out_head", 63, E)])
+    ("v_token", -1, E), ("lse_token", 7, E), ("lse_head", -1, E), ("out_sequence", -1, E), ("q_token", 511, E), ("k_head", 63, E), ("out_head", 63, E)])
 def test_attention_problems(name, field, value, status):
     c = Call(name)
     if field == "heads" and value == 514:
@@ -300,6 +300,7 @@ def test_backward_tensors():
     q, k, lse = t(2, 5, 4, 8), t(2, 7, 2, 8), t(2, 5, 4, dtype=torch.float32)
     b = hc.attention_backward
     refused(b, q, k, k, q, lse.bfloat16(), q, part="lse")
+    refused(b, q, k, k, q, lse[..., :1].expand(2, 5, 4), q, part="lse")
     refused(b, q, k, k, q, lse[:, :4], q, part="lse")
     refused(b, q, k, k, q[:, :4], lse, q, part="out")
     refused(b, q, k, k, q, lse, t(2, 5, 1, 8).expand(2, 5, 4, 8), part="d_out")

@@ -99,6 +99,38 @@ def test_packed_sequences_with_other_key_lengths(dt):
         check(q, k, v, f"{dt} {causal}", ql=ql, kl=kl, causal=causal)
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("dim", [64, 72, 31])
+def test_layouts(dt, dim):
+    """Columns of a merged projection (odd paddings make them unaligned), heads before tokens, tokens before sequences; the
+    gradients into columns of one merged tensor; statistics of another layout."""
+    b, n, heads, kv = 2, 150, 4, 2
+    t = T_OF[dt]
+    for pad in (0, 8, 1):
+        width = (heads + 2 * kv) * dim + pad
+        qkv = rand((b, n, width), t, 3)
+        grad = rand((b, n, width), t, 4)
+
+        def columns(x):
+            c = [x[..., i * dim:j * dim].view(b, n, j - i, dim) for i, j in ((0, heads), (heads, heads + kv), (heads + kv, heads + 2 * kv))]
+            return c
+        q, k, v = columns(qkv)
+        out, lse = check(q, k, v, f"{dt} {dim} merged {pad}", window=70, sinks=3)
+        do = rand((b, n, heads, dim), t, 5)
+        want = hc.attention_backward(q, k, v, out, lse, do)
+        rest = grad[..., (heads + 2 * kv) * dim:].clone()
+        odd = torch.empty(heads, n, b, device="cuda").permute(2, 1, 0)
+        odd.copy_(lse)
+        got = hc.attention_backward(q, k, v, out, odd, do, grads=columns(grad))
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+        assert torch.equal(torch.cat([x.flatten(2) for x in want], 2), grad[..., :(heads + 2 * kv) * dim])
+        assert torch.equal(rest, grad[..., (heads + 2 * kv) * dim:])
+    q, k, v = (rand((b, h, n, dim), t, 6 + h).transpose(1, 2) for h in (heads, kv, kv))
+    check(q, k, v, f"{dt} {dim} heads first", causal=False)
+    q, k, v = (rand((n, h, b, dim), t, 6 + h).permute(2, 0, 1, 3) for h in (heads, kv, kv))
+    check(q, k, v, f"{dt} {dim} sequences last")
+
+
 # ---------------------------------------------------------------- the cache in pages
 
 def cache(dt, lens, kv, dim, page, seed=5, spare=3):
@@ -145,6 +177,35 @@ def test_paged_head_sizes(dt, dim):
 @pytest.mark.parametrize("heads,kv", [(1, 1), (5, 1), (16, 1), (17, 1), (40, 2), (7, 7), (64, 2)])
 def test_paged_heads(dt, heads, kv):
     check_paged(dt, [130, 700], heads, kv, 128, 16)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_paged_layouts(dt):
+    """Both caches in one tensor, heads before rows, queries as columns of a merged projection; a table wider than needed;
+    pages that the cache does not have."""
+    lens, heads, kv, dim, page = [100, 33, 1], 8, 4, 64, 16
+    kc, vc, table, n = cache(dt, lens, kv, dim, page)
+    t = T_OF[dt]
+    for shift in (0, 1):
+        merged = rand((len(lens), heads * dim + 24 + shift), t, 9)
+        q = merged[:, shift:shift + heads * dim].view(len(lens), heads, dim)
+        want = ref.paged(q, kc, vc, table, n)
+        within(hc.paged_attention(q, kc, vc, table, n), *want, f"merged {dt} {shift}")
+        both = torch.empty(2, kc.shape[0], kv, page, dim, dtype=t, device="cuda").transpose(2, 3)
+        both[0], both[1] = kc, vc
+        wide = torch.full((len(lens), 40), 1 << 30, dtype=torch.int32, device="cuda")
+        wide[:, 3:3 + table.shape[1]] = table
+        out = torch.zeros(len(lens), heads, dim + 8, dtype=t, device="cuda")
+        hc.paged_attention(q, both[0], both[1], wide[:, 3:30], n, out=out[:, :, :dim])
+        within(out[:, :, :dim], *want, f"heads first {dt} {shift}")
+        assert not out[:, :, dim:].any()
+    for bad in (-1, -2 ** 31, kc.shape[0], 2 ** 31 - 1):
+        wrong = table.clone()
+        wrong[0, 2], wrong[1, 0], wrong[2, 0] = bad, bad, bad
+        within(hc.paged_attention(q, kc, vc, wrong, n), *ref.paged(q, kc, vc, wrong, n), f"bad page {bad}")
+    for length in (-5, 2 ** 31 - 1):
+        m = torch.tensor([100, length, 7], dtype=torch.int32, device="cuda")
+        within(hc.paged_attention(q, kc, vc, table, m), *ref.paged(q, kc, vc, table, m), f"length {length}")
 
 
 @pytest.mark.parametrize("dt", TYPES)
