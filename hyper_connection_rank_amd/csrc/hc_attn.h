@@ -32,7 +32,7 @@ struct AttnArgs {
   const void* d_out;
   void *dq, *dk, *dv;
   Strides3 sdo, sdq, sdk, sdv;
-  float* delta;                // [rows of q][heads]
+  float* stats;                // [2][heads][rows of q]: what a row's scores and dP start from (see hc_attn_bwd.hip)
   // split over the keys
   float* partial;
   int splits;
@@ -163,8 +163,7 @@ template <DT D> __device__ __forceinline__ typename Piece<D>::type piece_of(cons
   }
 }
 
-// Stages tiles of R rows by THREADS threads. Rows of the tile are rows of a tensor [tokens, heads, dim] at one
-// head (G = 1) or the packed rows of a key head's G heads.
+// Stages tiles of R rows (tokens of one head) by THREADS threads.
 template <DT D, int NB, int R, int THREADS, bool ALN> struct Stager {
   typedef Rows<D, NB> T;
   static constexpr int NL = R * T::CPR / THREADS;  // chunks of a thread
@@ -178,29 +177,36 @@ template <DT D, int NB, int R, int THREADS, bool ALN> struct Stager {
     const int r = row(i, tid);
     return (((i * THREADS + tid) % T::CPR) ^ T::swz(r)) * T::EPC;
   }
-  // Aligned: loads that write LDS. base: the tile's first row (the same in every lane); off(r): bytes of row r from there;
-  // n: rows that exist; the others, and columns from dim on, become zeros.
-  template <typename Off>
-  static __device__ __forceinline__ void load(const void* base, Off off, int n, int dim, uint32_t lds, int tid) {
-    static_assert(ALN, "aligned rows");
-    const u32x4 d = raw_desc(base);
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Aligned: loads that write LDS, of rows ld bytes apart. The rows that do not exist lie behind the descriptor's end and
+  // become zeros, as do columns from dim on, whose offset is behind every end. The offsets are those of the
+  // first chunks; the chunks after them lie whole rows further, with the same permutation.
+  static constexpr int SAME = THREADS / T::CPR % 16 == 0 ? 1 : 16 * T::CPR / THREADS;  // chunks until the permutation repeats
+  uint32_t off[SAME > NL ? NL : SAME];
+  __device__ __forceinline__ void init(uint32_t ld, int dim, int tid) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
+    for (int i = 0; i < (SAME > NL ? NL : SAME); ++i) {
       const int r = row(i, tid), c = col(i, tid);
-      const uint32_t o = r < n && c < dim ? off(r) + (uint32_t)(c * T::ES) : OUTSIDE;
-      lds_load<16, false>(d, o, __builtin_amdgcn_readfirstlane(lds + (i * THREADS + wave * 64) * 16));
+      off[i] = c < dim ? (uint32_t)r * ld + (uint32_t)(c * T::ES) : OUTSIDE;
     }
   }
+  // n: rows that exist from base on (the same in every lane).
+  __device__ __forceinline__ void load(const void* base, uint32_t ld, int n, int dim, uint32_t lds, int wave) const {
+    static_assert(ALN, "aligned rows");
+    const uint32_t bytes = n > 0 ? (uint32_t)(min(n, R) - 1) * ld + (uint32_t)(dim * T::ES) : 0u;
+    const u32x4 d = raw_desc(base, bytes);
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      lds_load<16, false>(d, off[i % SAME] + (uint32_t)(i / SAME * (SAME * THREADS / T::CPR)) * ld,
+                          __builtin_amdgcn_readfirstlane(lds + (i * THREADS + wave * 64) * 16));
+  }
   // Rows at any address, through registers.
-  template <typename Off>
-  static __device__ __forceinline__ void fetch(const void* base, Off off, int n, int dim, int tid, uint4* v) {
+  static __device__ __forceinline__ void fetch(const void* base, int64_t ld, int n, int dim, int tid, uint4* v) {
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int r = row(i, tid), c = col(i, tid), left = dim - c;
       v[i] = make_uint4(0u, 0u, 0u, 0u);
       if (r < n && left > 0) {
-        const elem_t* p = (const elem_t*)((const char*)base + off(r)) + c;
+        const elem_t* p = (const elem_t*)((const char*)base + r * ld) + c;
         if (left >= T::EPC) {
           v[i] = ld16<D, false>(p);
         } else {

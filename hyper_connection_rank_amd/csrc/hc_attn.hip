@@ -27,7 +27,7 @@ template <DT D> constexpr float weight_shift() { return D == DT::F16 ? 7.0f : 0.
 constexpr float LAG = 8.0f;
 
 template <DT D, int NB, bool ALN>
-__global__ __launch_bounds__(256, 1) void k_attention(const AttnArgs a) {
+__global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? 2 : 1)) void k_attention(const AttnArgs a) {
   typedef FwdShape<D, NB> F;
   typedef Rows<D, NB> T;
   typedef typename T::piece piece;
@@ -157,15 +157,16 @@ __global__ __launch_bounds__(256, 1) void k_attention(const AttnArgs a) {
   const uint32_t ldk = (uint32_t)(a.sk.t * T::ES), ldv = (uint32_t)(a.sv.t * T::ES);
   auto k_at = [&](int j0) { return kp + (int64_t)j0 * a.sk.t * T::ES; };
   auto v_at = [&](int j0) { return vp + (int64_t)j0 * a.sv.t * T::ES; };
-  auto k_off = [&](int r) { return (uint32_t)r * ldk; };
-  auto v_off = [&](int r) { return (uint32_t)r * ldv; };
   if constexpr (ALN) {
     const uint32_t l0 = lds_offset(lds);
+    S ks, vs;
+    ks.init(ldk, a.dim, tid);
+    vs.init(ldv, a.dim, tid);
     auto stage = [&](int i) {
       const int j0 = tiles(i) * KT, n = s.kl - j0;
       const uint32_t to = l0 + (i & 1) * 2 * S::BYTES;
-      S::load(k_at(j0), k_off, n, a.dim, to, tid);
-      S::load(v_at(j0), v_off, n, a.dim, to + S::BYTES, tid);
+      ks.load(k_at(j0), ldk, n, a.dim, to, wave);
+      vs.load(v_at(j0), ldv, n, a.dim, to + S::BYTES, wave);
     };
     if (tiles.count > 0) stage(0);
     for (int i = 0; i < tiles.count; ++i) {
@@ -180,8 +181,8 @@ __global__ __launch_bounds__(256, 1) void k_attention(const AttnArgs a) {
     uint4 fk[S::NL], fv[S::NL];
     auto fetch = [&](int i) {
       const int j0 = tiles(i) * KT, n = s.kl - j0;
-      S::fetch(k_at(j0), k_off, n, a.dim, tid, fk);
-      S::fetch(v_at(j0), v_off, n, a.dim, tid, fv);
+      S::fetch(k_at(j0), ldk, n, a.dim, tid, fk);
+      S::fetch(v_at(j0), ldv, n, a.dim, tid, fv);
     };
     if (tiles.count > 0) fetch(0);
     for (int i = 0; i < tiles.count; ++i) {

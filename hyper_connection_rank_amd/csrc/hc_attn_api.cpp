@@ -110,7 +110,8 @@ bool aligned16(std::initializer_list<const View*> all) {
   return true;
 }
 
-hc::Strides3 strides(const View& v) { return {v.s[0], v.s[1], v.s[2]}; }
+// Strides for the kernels. Rows behind a tensor's only one are told from it by their offset, so they have one.
+hc::Strides3 strides(const View& v) { return {v.s[0], v.n[1] > 1 ? v.s[1] : HCLRMIX_ATTENTION_MAX_DIM, v.s[2]}; }
 
 hclrmix_status check_ints(const char* name, const void* p) {
   return (uintptr_t)p & 3u ? fail(HCLRMIX_ERR_UNSUPPORTED, "%s must be 4-byte aligned", name) : HCLRMIX_OK;
@@ -349,7 +350,7 @@ hclrmix_status hclrmix_attention_backward(const void* q, const void* k, const vo
   a.sdq = strides(wq);
   a.sdk = strides(wk);
   a.sdv = strides(wv);
-  a.delta = (float*)((char*)workspace + HCLRMIX_COUNTER_BYTES);
+  a.stats = (float*)((char*)workspace + HCLRMIX_COUNTER_BYTES);
   (void)hipGetLastError();
   return done(hc::launch_attention_backward(a, p.dtype, aligned16({&vq, &vk, &vv, &vo, &vg, &wq, &wk, &wv}), (hipStream_t)stream));
 }

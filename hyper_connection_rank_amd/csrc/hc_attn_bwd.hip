@@ -17,6 +17,8 @@
 #include "hc_internal.h"
 
 #include <algorithm>
+#include <type_traits>
+#include <stdlib.h>
 
 namespace hc {
 
@@ -48,6 +50,11 @@ template <DT D> struct ColumnScale {
   }
   __device__ __forceinline__ float undo() const { return D == DT::F16 ? 1.0f / by : 1.0f; }
 };
+
+// Rows of q in all sequences; dkv's fp16 weights are taken 2^15 times as large: at most 2^15, and few below fp16's
+// normal numbers.
+__device__ __forceinline__ int64_t all_rows(const AttnArgs& a) { return a.q_starts ? a.q_tokens : a.batch * a.q_tokens; }
+template <DT D> constexpr float weight_up() { return D == DT::F16 ? 15.0f : 0.0f; }
 
 __device__ __forceinline__ void clear(f32x16& x) {
 #pragma unroll
@@ -113,9 +120,13 @@ __global__ __launch_bounds__(256, 1) void k_attention_dq(const AttnArgs a) {
     }
   }
   delta = halves_sum(delta);
-  const int64_t stat = ((a.q_starts ? s.q0 : s.b * a.q_tokens) + tok) * a.heads + h0 + g;
-  if (lane < 32 && mine < rows) a.delta[stat] = delta;
-  const float lse2 = a.lse[base_of(a.sl, false, h0 + g) + tok * a.sl.t] * LOG2E;
+  const float lse = a.lse[base_of(a.sl, false, h0 + g) + tok * a.sl.t], lse2 = lse * LOG2E;
+  if (lane < 32 && mine < rows) {
+    // For k_attention_dkv. A row that sees nothing weighs nothing there.
+    float* const to = a.stats + (h0 + g) * all_rows(a) + (a.q_starts ? s.q0 : s.b * a.q_tokens) + tok;
+    *to = lse == NEG_INF ? NEG_INF : (weight_up<D>() * LN2 - lse) / a.scale;
+    to[a.heads * all_rows(a)] = -delta;
+  }
   const Sees see = sees(a, tok + off, s.kl);
   const Sees wg_first = sees(a, r0 / a.group + off, s.kl);
   const Sees wg_last = sees(a, min(r0 + F::TR - 1, rows - 1) / a.group + off, s.kl);
@@ -161,15 +172,16 @@ __global__ __launch_bounds__(256, 1) void k_attention_dq(const AttnArgs a) {
   const uint32_t ldk = (uint32_t)(a.sk.t * T::ES), ldv = (uint32_t)(a.sv.t * T::ES);
   auto k_at = [&](int j0) { return kp + (int64_t)j0 * a.sk.t * T::ES; };
   auto v_at = [&](int j0) { return vp + (int64_t)j0 * a.sv.t * T::ES; };
-  auto k_off = [&](int j) { return (uint32_t)j * ldk; };
-  auto v_off = [&](int j) { return (uint32_t)j * ldv; };
   if constexpr (ALN) {
     const uint32_t l0 = lds_offset(lds);
+    S ks, vs;
+    ks.init(ldk, a.dim, tid);
+    vs.init(ldv, a.dim, tid);
     auto stage = [&](int i) {
       const int j0 = tiles(i) * KT, n = s.kl - j0;
       const uint32_t to = l0 + (i & 1) * 2 * S::BYTES;
-      S::load(k_at(j0), k_off, n, a.dim, to, tid);
-      S::load(v_at(j0), v_off, n, a.dim, to + S::BYTES, tid);
+      ks.load(k_at(j0), ldk, n, a.dim, to, wave);
+      vs.load(v_at(j0), ldv, n, a.dim, to + S::BYTES, wave);
     };
     if (tiles.count > 0) stage(0);
     for (int i = 0; i < tiles.count; ++i) {
@@ -183,8 +195,8 @@ __global__ __launch_bounds__(256, 1) void k_attention_dq(const AttnArgs a) {
     uint4 fk[S::NL], fv[S::NL];
     auto fetch = [&](int i) {
       const int j0 = tiles(i) * KT, n = s.kl - j0;
-      S::fetch(k_at(j0), k_off, n, a.dim, tid, fk);
-      S::fetch(v_at(j0), v_off, n, a.dim, tid, fv);
+      S::fetch(k_at(j0), ldk, n, a.dim, tid, fk);
+      S::fetch(v_at(j0), ldv, n, a.dim, tid, fv);
     };
     if (tiles.count > 0) fetch(0);
     for (int i = 0; i < tiles.count; ++i) {
@@ -213,27 +225,32 @@ __global__ __launch_bounds__(256, 1) void k_attention_dq(const AttnArgs a) {
 
 // ------------------------------------------------------------------ dk and dv
 
-// NBO: blocks of 32 columns of dk and dv that one workgroup sums (all, or half where the registers hold no more).
-template <DT D, int NB> struct DkvShape {
+// WK: blocks of 32 keys of a workgroup; its four waves are WK of them times WR shares of the rows, whose sums are added at the
+// end. NBO: blocks of 32 columns of dk and dv that one workgroup sums (all, or half where the registers hold no more).
+template <DT D, int NB, int WK> struct DkvShape {
   typedef Rows<D, NB> T;
-  static constexpr int QT = T::RB >= 512 ? 32 : 64, WAVES = 4, TK = 32 * WAVES;
+  static constexpr int WR = 4 / WK, TK = 32 * WK;
+  static constexpr int QT = T::RB >= 512 && WR == 1 ? 32 : 64;
   static constexpr int NBO = NB == 8 ? 4 : NB, HALVES = NB / NBO;
+  static constexpr int NST = 2 * QT * T::RB * 3 <= 131072 ? 3 : 2;  // buffers of q and d_out
 };
 
-template <DT D, int NB, bool ALN>
+template <DT D, int NB, int WK, bool ALN>
 __global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
-  typedef DkvShape<D, NB> F;
+  typedef DkvShape<D, NB, WK> F;
   typedef Rows<D, NB> T;
   typedef typename T::piece piece;
-  constexpr int QT = F::QT, THREADS = 64 * F::WAVES, NBO = F::NBO;
+  constexpr int QT = F::QT, THREADS = 256, NBO = F::NBO, WR = F::WR;
   constexpr int STEPS = 32 * NB / T::STEP, PSTEPS = 32 / T::STEP;
   typedef Stager<D, NB, QT, THREADS, ALN> S;
-  constexpr int GONE = -(1 << 30);  // the position of rows that do not exist
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[4 * S::BYTES];
-  __shared__ __attribute__((aligned(16))) float row_lse[2][QT], row_delta[2][QT];
-  __shared__ __attribute__((aligned(16))) int row_pos[2][QT];
-  static_assert(F::WAVES * 32 * T::RB <= 4 * S::BYTES, "the results fit the staging buffers");
+  constexpr int NST = ALN ? F::NST : 2;
+  // Buffers of q and d_out, then of what the sums of a row start from: of s, of dP (one array: the loads that fill it are not
+  // stores to the compiler, which takes an array without stores for undefined).
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[NST * (2 * S::BYTES + 1024)];
+  float (*const row_stats)[4][64] = (float (*)[4][64])(lds + NST * 2 * S::BYTES);
+  static_assert(WK * 32 * T::RB <= 4 * S::BYTES && (WR == 1 || WK * NBO * 4096 <= 4 * S::BYTES), "the results fit the staging buffers");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+  const int wk = wave % WK, wr = wave / WK;
 
   int id = blockIdx.x;
   const int d0 = F::HALVES > 1 ? id % F::HALVES * NBO : 0;
@@ -246,9 +263,11 @@ __global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
     return (keys ? (a.k_starts ? s.k0 * st.t : s.b * st.b) : (a.q_starts ? s.q0 * st.t : s.b * st.b)) + head * st.h;
   };
   const int h0 = kvh * a.group, off = s.kl - s.ql;
-  const int jw = j0 + wave * 32, j = jw + (lane & 31);  // the wave's first key and this lane's
+  const int jw = j0 + wk * 32, j = jw + (lane & 31);  // the wave's first key and this lane's
 
-  // The rows that see any of these keys: positions p_lo .. p_hi.
+  // The queries t_lo .. t_end - 1 see keys of this tile. Tiles of QT of them of one head, the heads of the last queries
+  // first: workgroups of neighbouring tiles of keys, which run at the same time on one XCD, begin with the same rows
+  // and stay together, so that its L2 serves all of them.
   const int j_last = min(j0 + F::TK, s.kl) - 1;
   int p_lo = off, p_hi = s.kl - 1;
   if (a.causal) p_lo = max(p_lo, j0);
@@ -256,12 +275,12 @@ __global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
     p_hi = min(p_hi, j_last + a.window - 1);
     if (!a.causal) p_lo = max(p_lo, j0 - a.window + 1);
   }
-  const int r_begin = (p_lo - off) * a.group, r_end = p_hi < p_lo ? r_begin : (p_hi - off + 1) * a.group;
-  const int count = (r_end - r_begin + QT - 1) / QT;
+  const int t_lo = p_lo - off, t_end = p_hi - off + 1;
+  const int per_head = t_end > t_lo ? (t_end - t_lo + QT - 1) / QT : 0, count = per_head * a.group;
 
   piece kf[STEPS], vf[STEPS];
   {
-    const int jc = min(j, s.kl - 1);
+    const int jc = min(j, s.kl - 1);  // keys past the last one repeat it and are not written
     const char* pk = (const char*)a.k + (base_of(a.sk, true, kvh) + jc * a.sk.t) * T::ES;
     const char* pv = (const char*)a.v + (base_of(a.sv, true, kvh) + jc * a.sv.t) * T::ES;
 #pragma unroll
@@ -278,51 +297,44 @@ __global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
   }
   ColumnScale<D> scale;
   const float c = a.scale * LOG2E;
-  constexpr float UP = D == DT::F16 ? 15.0f : 0.0f;  // fp16 weights 2^15 times as large, at most 2^15
 
-  auto multiply = [&](const unsigned char* qt, const unsigned char* gt, int buf, int r0) {
+  auto multiply = [&](const unsigned char* qt, const unsigned char* gt, int buf, int t0) {
 #pragma unroll
-    for (int b = 0; b < QT / 32; ++b) {
-      const int ra = r0 + 32 * b, rz = min(ra + 32, r_end) - 1;
-      if (ra >= r_end) continue;
-      const int pa = ra / a.group + off, pz = rz / a.group + off;  // the block's first and last positions
-      const int jz = jw + 31;
-      if (a.causal && pz < jw) continue;
+    for (int bb = 0; bb < QT / 32; bb += WR) {
+      const int b = bb + wr;
+      const int ta = t0 + 32 * b, pa = ta + off, pz = min(ta + 32, t_end) - 1 + off, jz = jw + 31;
+      if (ta >= t_end || (a.causal && pz < jw)) continue;
       if (a.window && jw >= a.sinks && (jz <= pa - a.window || (!a.causal && jw >= pz + a.window))) continue;
-      if (jw >= s.kl) continue;
-      const bool whole = ra + 32 <= r_end && jz < s.kl && (!a.causal || jz <= pa) &&
+      const bool whole = (!a.causal || jz <= pa) &&
                          (!a.window || (jw > pz - a.window && (a.causal || jz < pa + a.window)) || jz < a.sinks);
+      // The sums start from what is subtracted in any case: s - lse, over the scale, and dP - delta.
       f32x16 x, y;
-      clear(x);
-      clear(y);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const f32x4 sl = *(const f32x4*)&row_stats[buf][0][32 * b + 8 * u + 4 * h];
+        const f32x4 dl = *(const f32x4*)&row_stats[buf][1][32 * b + 8 * u + 4 * h];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[4 * u + e] = sl[e];
+          y[4 * u + e] = dl[e];
+        }
+      }
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) x = mfma32<D>(T::direct(qt, 32 * b, i, lane), kf[i], x);
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) y = mfma32<D>(T::direct(gt, 32 * b, i, lane), vf[i], y);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const f32x4 nl = *(const f32x4*)&row_lse[buf][32 * b + 8 * u + 4 * h];
-        const f32x4 dl = *(const f32x4*)&row_delta[buf][32 * b + 8 * u + 4 * h];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(x[4 * u + e], c, UP - nl[e]));
-          x[4 * u + e] = p;
-          y[4 * u + e] = p * (y[4 * u + e] - dl[e]) * (D == DT::F16 ? 0x1p-15f : 1.0f);
-        }
+      for (int e = 0; e < 16; ++e) {
+        x[e] = __builtin_amdgcn_exp2f(x[e] * c);
+        y[e] = x[e] * y[e];
       }
       if (!whole) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int4 pos = *(const int4*)&row_pos[buf][32 * b + 8 * u + 4 * h];
-          const int pp[4] = {pos.x, pos.y, pos.z, pos.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int p = pp[e], far = p - j;
-            const bool in = p > GONE && j < s.kl && (!a.causal || far >= 0) &&
-                            (!a.window || (far < a.window && far > -a.window) || j < a.sinks);
-            x[4 * u + e] = in ? x[4 * u + e] : 0.0f;
-            y[4 * u + e] = in ? y[4 * u + e] : 0.0f;
-          }
+        for (int e = 0; e < 16; ++e) {
+          const int far = pa + 8 * (e >> 2) + 4 * h + (e & 3) - j;
+          const bool in = (!a.causal || far >= 0) && (!a.window || (far < a.window && far > -a.window) || j < a.sinks);
+          x[e] = in ? x[e] : 0.0f;
+          y[e] = in ? y[e] : 0.0f;
         }
       }
 #pragma unroll
@@ -341,108 +353,108 @@ __global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
     }
   };
 
-  // This thread's rows of the tile being loaded: query and head of each, QT rows further with every tile.
-  const int step_t = QT / a.group, step_g = QT - step_t * a.group;
-  int tk[S::NL], hd[S::NL], st_t, st_g;
-#pragma unroll
-  for (int i = 0; i < S::NL; ++i) {
-    const int r = r_begin + S::row(i, tid);
-    tk[i] = r / a.group;
-    hd[i] = r - tk[i] * a.group;
-  }
-  st_t = (r_begin + (tid & (QT - 1))) / a.group;
-  st_g = r_begin + (tid & (QT - 1)) - st_t * a.group;
-  auto advance = [&](int& tok, int& g) {
-    tok += step_t;
-    g += step_g;
-    if (g >= a.group) {
-      g -= a.group;
-      ++tok;
-    }
-  };
-  const int t_end = p_hi - off + 1;  // queries before this one
+  const uint32_t ldq = (uint32_t)(a.sq.t * T::ES), ldg = (uint32_t)(a.sdo.t * T::ES);
   const char* qp = (const char*)a.q + base_of(a.sq, false, h0) * T::ES;
   const char* gp = (const char*)a.d_out + base_of(a.sdo, false, h0) * T::ES;
-  const int64_t stat0 = (a.q_starts ? s.q0 : s.b * a.q_tokens) * a.heads + h0;
-  const int64_t lse0 = base_of(a.sl, false, h0);
-  float n_lse = 0.0f, n_delta = 0.0f;
-  int n_pos = GONE;
-  auto fetch_stats = [&]() {  // of the next tile, into registers
-    const bool in = st_t < t_end;
-    const int64_t at = stat0 + (int64_t)(in ? st_t : 0) * a.heads + st_g;
-    n_lse = in ? a.lse[lse0 + st_t * a.sl.t + st_g * a.sl.h] * LOG2E : 0.0f;
-    n_delta = in ? a.delta[at] : 0.0f;
-    n_pos = in ? st_t + off : GONE;
-    advance(st_t, st_g);
+  const float* const stats = a.stats + h0 * all_rows(a) + (a.q_starts ? s.q0 : s.b * a.q_tokens);
+  // Statistic w (0: of s, 1: of dP) of a tile's rows; rows past the last one have zeros, as their q and d_out.
+  auto stats_at = [&](int w, int g, int t) { return stats + (w * a.heads + g) * all_rows(a) + t; };
+  struct Place {
+    int g, t;
   };
-  auto put_stats = [&](int buf) {
-    if (tid < QT) {
-      row_lse[buf][tid] = n_lse;
-      row_delta[buf][tid] = n_delta;
-      row_pos[buf][tid] = n_pos;
+  auto next = [&](Place& p) {
+    if (++p.g == a.group) {
+      p.g = 0;
+      p.t -= QT;
     }
   };
+  auto q_at = [&](const Place& p) { return qp + (p.t * a.sq.t + p.g * a.sq.h) * T::ES; };
+  auto g_at = [&](const Place& p) { return gp + (p.t * a.sdo.t + p.g * a.sdo.h) * T::ES; };
+  const int t_last = t_lo + (per_head - 1) * QT;
+  Place here{0, t_last}, ahead{0, t_last};  // the tile in work, and the next to load
   if constexpr (ALN) {
     const uint32_t l0 = lds_offset(lds);
-    auto stage = [&](int buf) {
-#pragma unroll
-      for (int i = 0; i < S::NL; ++i) {
-        const int col = S::col(i, tid);
-        const bool in = tk[i] < t_end && col < a.dim;
-        const char* pq = in ? qp + (tk[i] * a.sq.t + hd[i] * a.sq.h + col) * T::ES : (const char*)zeros16;
-        const char* pg = in ? gp + (tk[i] * a.sdo.t + hd[i] * a.sdo.h + col) * T::ES : (const char*)zeros16;
-        const uint32_t to = __builtin_amdgcn_readfirstlane(l0 + buf * 2 * S::BYTES + (i * THREADS + wave * 64) * 16);
-        lds_load_from(pq, to);
-        lds_load_from(pg, to + S::BYTES);
-        advance(tk[i], hd[i]);
-      }
+    S qs, gs;
+    qs.init(ldq, a.dim, tid);
+    gs.init(ldg, a.dim, tid);
+    const int w = min(wave, 2);  // waves 2 and 3 load nothing, so that all waves have as many loads in flight
+    constexpr int LOADS = 2 * S::NL + 1;
+    auto stage = [&](int buf, bool in) {
+      const uint32_t to = l0 + buf * 2 * S::BYTES;
+      const int n = in ? t_end - ahead.t : 0;
+      qs.load(q_at(ahead), ldq, n, a.dim, to, wave);
+      gs.load(g_at(ahead), ldg, n, a.dim, to + S::BYTES, wave);
+      lds_load<4, false>(raw_desc(stats_at(w & 1, ahead.g, ahead.t), w < 2 && n > 0 ? 4 * min(n, QT) : 0), 4 * lane,
+                         __builtin_amdgcn_readfirstlane(lds_offset(&row_stats[buf][wave][0])));
+      if (in) next(ahead);
     };
-    if (count > 0) {
-      fetch_stats();
-      put_stats(0);
-      if (count > 1) fetch_stats();
-      stage(0);
-    }
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) stage(i, i < count);
+    int buf = 0;
     for (int i = 0; i < count; ++i) {
-      // Tile i and the next tile's statistics have arrived; every wave is done with tile i - 1.
-      wait_loads<0>();
+      // Tile i has arrived; every wave is done with tile i - 1, whose buffer the next tile to load fills.
+      wait_loads<(NST - 2) * LOADS>();
       lds_barrier();
-      if (i + 1 < count) {
-        put_stats((i + 1) & 1);
-        fetch_stats();
-        stage((i + 1) & 1);
-      }
-      const unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
-      multiply(cur, cur + S::BYTES, i & 1, r_begin + i * QT);
+      stage(buf == 0 ? NST - 1 : buf - 1, i + NST - 1 < count);
+      const unsigned char* cur = lds + buf * 2 * S::BYTES;
+      multiply(cur, cur + S::BYTES, buf, here.t);
+      next(here);
+      buf = buf == NST - 1 ? 0 : buf + 1;
     }
+    wait_loads<0>();  // LDS must not be given up with loads into it in flight
   } else {
     uint4 fq[S::NL], fg[S::NL];
+    float fs = 0.0f;
     auto fetch = [&]() {
-      fetch_stats();
-#pragma unroll
-      for (int i = 0; i < S::NL; ++i) {
-        fq[i] = fg[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (tk[i] < t_end) {
-          fq[i] = chunk16<D, false>(qp + (tk[i] * a.sq.t + hd[i] * a.sq.h) * T::ES, S::col(i, tid), a.dim);
-          fg[i] = chunk16<D, false>(gp + (tk[i] * a.sdo.t + hd[i] * a.sdo.h) * T::ES, S::col(i, tid), a.dim);
-        }
-        advance(tk[i], hd[i]);
-      }
+      S::fetch(q_at(ahead), ldq, t_end - ahead.t, a.dim, tid, fq);
+      S::fetch(g_at(ahead), ldg, t_end - ahead.t, a.dim, tid, fg);
+      fs = wave < 2 && lane < min(QT, t_end - ahead.t) ? stats_at(wave, ahead.g, ahead.t)[lane] : 0.0f;
+      next(ahead);
     };
     if (count > 0) fetch();
     for (int i = 0; i < count; ++i) {
       unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
       S::put(cur, tid, fq);
       S::put(cur + S::BYTES, tid, fg);
-      put_stats(i & 1);
+      row_stats[i & 1][wave][lane] = fs;
       lds_barrier();
       if (i + 1 < count) fetch();
-      multiply(cur, cur + S::BYTES, i & 1, r_begin + i * QT);
+      multiply(cur, cur + S::BYTES, i & 1, here.t);
+      next(here);
     }
   }
   lds_barrier();
 
-  unsigned char* const rows32 = lds + wave * 32 * T::RB;
+  if constexpr (WR == 2) {
+    // The second share's sums to the first's, through LDS: 16 bytes of every lane at a time.
+    const float to_one = D == DT::F16 ? 1.0f / scale.by : 1.0f;  // each share has its own power of two
+    auto join = [&](f32x16 (&sum)[NBO], float f) {
+      f32x4* const at = (f32x4*)lds + (wk * NBO * 4) * 64 + lane;
+      if (wr == 1) {
+#pragma unroll
+        for (int d = 0; d < NBO; ++d)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            at[(4 * d + u) * 64] = f32x4{sum[d][4 * u] * f, sum[d][4 * u + 1] * f, sum[d][4 * u + 2] * f, sum[d][4 * u + 3] * f};
+      }
+      lds_barrier();
+      if (wr == 0) {
+#pragma unroll
+        for (int d = 0; d < NBO; ++d)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const f32x4 v = at[(4 * d + u) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[d][4 * u + e] = sum[d][4 * u + e] * f + v[e];
+          }
+      }
+      lds_barrier();
+    };
+    join(dv, 1.0f);
+    join(dk, to_one);
+    if (wr != 0) return;
+  }
+  unsigned char* const rows32 = lds + wk * 32 * T::RB;
   auto write = [&](void* base, const Strides3& st, const f32x16 (&sum)[NBO], float f) {
     if (!base) return;
     rows_to_lds<D, NB>(rows32, sum, f, lane);
@@ -458,7 +470,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
   write(a.dv, a.sdv, dv, D == DT::F16 ? 0x1p-15f : 1.0f);
-  write(a.dk, a.sdk, dk, a.scale * scale.undo());
+  write(a.dk, a.sdk, dk, (D == DT::F16 ? 0x1p-15f : 1.0f) * (WR == 2 ? a.scale : a.scale * scale.undo()));
 }
 
 namespace {
@@ -476,10 +488,17 @@ template <DT D, int NB> hipError_t go(const AttnArgs& a0, bool aligned, hipStrea
     else hipLaunchKernelGGL((k_attention_dq<D, NB, false>), grid, block, 0, s, a);
   }
   if ((a.dk || a.dv) && a.k_tokens > 0) {
-    const int64_t n = tiles(a.k_starts, a.k_tokens, DkvShape<D, NB>::TK);
-    const dim3 grid((unsigned)(n * a.kv_heads * DkvShape<D, NB>::HALVES)), block(64 * DkvShape<D, NB>::WAVES);
-    if (aligned) hipLaunchKernelGGL((k_attention_dkv<D, NB, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_attention_dkv<D, NB, false>), grid, block, 0, s, a);
+    auto run = [&](auto wk) {
+      constexpr int WK = decltype(wk)::value;
+      typedef DkvShape<D, NB, WK> F;
+      const int64_t n = tiles(a.k_starts, a.k_tokens, F::TK);
+      const dim3 grid((unsigned)(n * a.kv_heads * F::HALVES)), block(256);
+      if (aligned) hipLaunchKernelGGL((k_attention_dkv<D, NB, WK, true>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((k_attention_dkv<D, NB, WK, false>), grid, block, 0, s, a);
+    };
+    if constexpr (Rows<D, NB>::RB >= 1024) run(std::integral_constant<int, 4>());
+    else if (getenv("WK4")) run(std::integral_constant<int, 4>());
+    else run(std::integral_constant<int, 2>());
   }
   return hipGetLastError();
 }
@@ -501,7 +520,7 @@ hipError_t launch_attention_backward(AttnArgs a, int dtype, bool aligned, hipStr
 }
 
 size_t attention_backward_scratch(const AttnArgs& a, int) {
-  return (size_t)(a.q_starts ? a.q_tokens : a.batch * a.q_tokens) * a.heads * sizeof(float);
+  return (size_t)(a.q_starts ? a.q_tokens : a.batch * a.q_tokens) * a.heads * 2 * sizeof(float);
 }
 
 }  // namespace hc

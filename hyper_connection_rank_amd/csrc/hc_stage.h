@@ -13,6 +13,12 @@ __device__ __forceinline__ u32x4 raw_desc(const void* base) {
   return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
                (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)), 0x7FFFFFF0u, 0x00020000u};
 }
+// The same with an end: what lies at `bytes` or behind reads as zeros.
+__device__ __forceinline__ u32x4 raw_desc(const void* base, uint32_t bytes) {
+  u32x4 d = raw_desc(base);
+  d[2] = (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes);
+  return d;
+}
 __device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(const lds_u8*)p; }
 // Lane l: W bytes (16 or 4) from offset off of the descriptor to LDS byte dst + W l (dst
 // the same in every lane). Written out because the compiler, which cannot tell the stage
