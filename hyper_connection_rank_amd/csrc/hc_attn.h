@@ -332,6 +332,14 @@ template <int KT> __device__ __forceinline__ KeyTiles key_tiles(const Sees& firs
   return t;
 }
 
+// Workgroups of descending work for compute units that hold several at once: every other round of 256 backwards, so that
+// what a unit gets evens out also where all are resident from the start. Eight neighbours stay together, one to an
+// XCD, so that each XCD keeps its key heads.
+__device__ __forceinline__ int snake(int id, int n) {
+  const int round = id >> 8, i = id & 255;
+  return (round & 1) && (round + 1) * 256 <= n ? (round << 8) | ((31 - (i >> 3)) << 3) | (i & 7) : id;
+}
+
 // The sequence of a workgroup and its place in it.
 struct Seq {
   int64_t q0, k0;  // first rows
@@ -343,8 +351,9 @@ struct Seq {
 __device__ __forceinline__ Seq find_sequence(const AttnArgs& a, const int* starts, int64_t tokens, int unit, int tr, int64_t t) {
   Seq s;
   if (!starts) {
-    s.b = (int)(t / a.tiles);
-    s.tile = (int)(t - (int64_t)s.b * a.tiles);
+    // The sequences' tiles in turn: they are of one size, so the ones with most work of all come first (or last).
+    s.tile = (int)(t / a.batch);
+    s.b = (int)(t - (int64_t)s.tile * a.batch);
     s.ql = (int)a.q_tokens;
     s.kl = (int)a.k_tokens;
     s.q0 = s.k0 = 0;  // the batch strides lead to the sequence

@@ -18,7 +18,6 @@
 
 #include <algorithm>
 #include <type_traits>
-#include <stdlib.h>
 
 namespace hc {
 
@@ -225,45 +224,51 @@ __global__ __launch_bounds__(256, 1) void k_attention_dq(const AttnArgs a) {
 
 // ------------------------------------------------------------------ dk and dv
 
-// WK: blocks of 32 keys of a workgroup; its four waves are WK of them times WR shares of the rows, whose sums are added at the
-// end. NBO: blocks of 32 columns of dk and dv that one workgroup sums (all, or half where the registers hold no more).
-template <DT D, int NB, int WK> struct DkvShape {
+// A workgroup's four waves take 32 keys each, whose rows of k and v a wave keeps as the products' second operands and whose
+// dk and dv it sums; q and d_out pass through LDS in tiles of QT rows. One wave issues an instruction every four cycles
+// at most, and waits for its LDS reads, so either two waves share a SIMD, or (where two do not fit the registers) a wave
+// works on RBW = 2 blocks of 32 rows at once, which fill each other's gaps.
+// NBO: blocks of 32 columns of dk and dv that one workgroup sums (all, or half where the registers hold no more).
+//
+// Few tiles of keys: the rows are split over `parts` workgroups, whose fp32 sums k_attention_join adds in order.
+template <DT D, int NB> struct DkvShape {
   typedef Rows<D, NB> T;
-  static constexpr int WR = 4 / WK, TK = 32 * WK;
-  static constexpr int QT = T::RB >= 512 && WR == 1 ? 32 : 64;
+  static constexpr int RBW = D != DT::F32 && NB == 4 ? 2 : 1, TK = 128, QT = 32 * RBW;
   static constexpr int NBO = NB == 8 ? 4 : NB, HALVES = NB / NBO;
-  static constexpr int NST = 2 * QT * T::RB * 3 <= 131072 ? 3 : 2;  // buffers of q and d_out
+  static constexpr int WAVES = D == DT::F32 ? (NB == 2 ? 2 : 1) : NB <= 3 ? 2 : 1;  // of a SIMD
 };
 
-template <DT D, int NB, int WK, bool ALN>
-__global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
-  typedef DkvShape<D, NB, WK> F;
+template <DT D, int NB, bool ALN>
+__global__ __launch_bounds__(256, (ALN ? DkvShape<D, NB>::WAVES : 1)) void k_attention_dkv(const AttnArgs a) {
+  typedef DkvShape<D, NB> F;
   typedef Rows<D, NB> T;
   typedef typename T::piece piece;
-  constexpr int QT = F::QT, THREADS = 256, NBO = F::NBO, WR = F::WR;
+  constexpr int QT = F::QT, THREADS = 256, NBO = F::NBO;
   constexpr int STEPS = 32 * NB / T::STEP, PSTEPS = 32 / T::STEP;
+  constexpr int RBW = F::RBW;
   typedef Stager<D, NB, QT, THREADS, ALN> S;
-  constexpr int NST = ALN ? F::NST : 2;
-  // Buffers of q and d_out, then of what the sums of a row start from: of s, of dP (one array: the loads that fill it are not
-  // stores to the compiler, which takes an array without stores for undefined).
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[NST * (2 * S::BYTES + 1024)];
-  float (*const row_stats)[4][64] = (float (*)[4][64])(lds + NST * 2 * S::BYTES);
-  static_assert(WK * 32 * T::RB <= 4 * S::BYTES && (WR == 1 || WK * NBO * 4096 <= 4 * S::BYTES), "the results fit the staging buffers");
+  // Two buffers of q and d_out, two of what the sums of a row start from: of s, of dP (one array: the loads that
+  // fill it are not stores to the compiler, which takes an array without stores for undefined).
+  constexpr int STATS = 4 * S::BYTES;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[STATS + 1024];
+  static_assert(4 * 32 * T::RB <= 4 * S::BYTES, "the results fit the staging buffers");
+  float (*const row_stats)[2][64] = (float (*)[2][64])(lds + STATS);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
-  const int wk = wave % WK, wr = wave / WK;
 
-  int id = blockIdx.x;
+  int id = snake(blockIdx.x, gridDim.x);
+  const int kvh = id % a.kv_heads;
+  id /= a.kv_heads;
   const int d0 = F::HALVES > 1 ? id % F::HALVES * NBO : 0;
   id /= F::HALVES;
-  const int kvh = id % a.kv_heads;
-  const Seq s = find_sequence(a, a.k_starts, a.k_tokens, 1, F::TK, id / a.kv_heads);
+  const int part = id % a.splits;
+  const Seq s = find_sequence(a, a.k_starts, a.k_tokens, 1, F::TK, id / a.splits);
   const int j0 = s.tile * F::TK;
   if (s.tile < 0 || j0 >= s.kl) return;
   auto base_of = [&](const Strides3& st, bool keys, int head) {
     return (keys ? (a.k_starts ? s.k0 * st.t : s.b * st.b) : (a.q_starts ? s.q0 * st.t : s.b * st.b)) + head * st.h;
   };
   const int h0 = kvh * a.group, off = s.kl - s.ql;
-  const int jw = j0 + wk * 32, j = jw + (lane & 31);  // the wave's first key and this lane's
+  const int jw = j0 + wave * 32, j = jw + (lane & 31);  // the wave's first key and this lane's
 
   // The queries t_lo .. t_end - 1 see keys of this tile. Tiles of QT of them of one head, the heads of the last queries
   // first: workgroups of neighbouring tiles of keys, which run at the same time on one XCD, begin with the same rows
@@ -276,7 +281,8 @@ __global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
     if (!a.causal) p_lo = max(p_lo, j0 - a.window + 1);
   }
   const int t_lo = p_lo - off, t_end = p_hi - off + 1;
-  const int per_head = t_end > t_lo ? (t_end - t_lo + QT - 1) / QT : 0, count = per_head * a.group;
+  const int per_head = t_end > t_lo ? (t_end - t_lo + QT - 1) / QT : 0, all = per_head * a.group;
+  const int i0 = (int)((int64_t)all * part / a.splits), count = (int)((int64_t)all * (part + 1) / a.splits) - i0;
 
   piece kf[STEPS], vf[STEPS];
   {
@@ -297,183 +303,239 @@ __global__ __launch_bounds__(256, 1) void k_attention_dkv(const AttnArgs a) {
   }
   ColumnScale<D> scale;
   const float c = a.scale * LOG2E;
+  // This lane's key is seen from p if p - j is at least low and less than span beyond.
+  const bool any = !a.window || j < a.sinks;
+  const int low = a.causal ? 0 : any ? -(1 << 30) : 1 - a.window;
+  const uint32_t span = any ? 0x7FFFFFFFu : (uint32_t)(a.window - low);
 
-  auto multiply = [&](const unsigned char* qt, const unsigned char* gt, int buf, int t0) {
+  // A tile whose queries start at t0. The sums start from what is subtracted in any case: s - lse, over the scale, and
+  // dP - delta.
+  auto multiply = [&](auto buffer, int t0) {
+    constexpr int buf = decltype(buffer)::value;
+    const unsigned char* const qt = lds + buf * 2 * S::BYTES;
+    const unsigned char* const gt = qt + S::BYTES;
+    const int pa = t0 + off, pz = pa + QT - 1, jz = jw + 31;
+    if (jw >= s.kl || (a.causal && pz < jw)) return;
+    if (a.window && jw >= a.sinks && (jz <= pa - a.window || (!a.causal && jw >= pz + a.window))) return;
+    const bool whole = (!a.causal || jz <= pa) &&
+                       (!a.window || (jw > pz - a.window && (a.causal || jz < pa + a.window)) || jz < a.sinks);
+    f32x16 x[RBW], y[RBW];
 #pragma unroll
-    for (int bb = 0; bb < QT / 32; bb += WR) {
-      const int b = bb + wr;
-      const int ta = t0 + 32 * b, pa = ta + off, pz = min(ta + 32, t_end) - 1 + off, jz = jw + 31;
-      if (ta >= t_end || (a.causal && pz < jw)) continue;
-      if (a.window && jw >= a.sinks && (jz <= pa - a.window || (!a.causal && jw >= pz + a.window))) continue;
-      const bool whole = (!a.causal || jz <= pa) &&
-                         (!a.window || (jw > pz - a.window && (a.causal || jz < pa + a.window)) || jz < a.sinks);
-      // The sums start from what is subtracted in any case: s - lse, over the scale, and dP - delta.
-      f32x16 x, y;
+    for (int b = 0; b < RBW; ++b)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const f32x4 sl = *(const f32x4*)&row_stats[buf][0][32 * b + 8 * u + 4 * h];
         const f32x4 dl = *(const f32x4*)&row_stats[buf][1][32 * b + 8 * u + 4 * h];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[4 * u + e] = sl[e];
-          y[4 * u + e] = dl[e];
+          x[b][4 * u + e] = sl[e];
+          y[b][4 * u + e] = dl[e];
         }
       }
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) x = mfma32<D>(T::direct(qt, 32 * b, i, lane), kf[i], x);
+    for (int b = 0; b < RBW; ++b)
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) y = mfma32<D>(T::direct(gt, 32 * b, i, lane), vf[i], y);
+      for (int i = 0; i < STEPS; ++i) x[b] = mfma32<D>(T::direct(qt, 32 * b, i, lane), kf[i], x[b]);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = __builtin_amdgcn_exp2f(x[e] * c);
-        y[e] = x[e] * y[e];
-      }
-      if (!whole) {
+    for (int b = 0; b < RBW; ++b)
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) y[b] = mfma32<D>(T::direct(gt, 32 * b, i, lane), vf[i], y[b]);
+#pragma unroll
+    for (int b = 0; b < RBW; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[b][e] = __builtin_amdgcn_exp2f(x[b][e] * c);
+    if (!whole) {
+      const uint32_t from = (uint32_t)(pa + 4 * h - j - low);
+#pragma unroll
+      for (int b = 0; b < RBW; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int far = pa + 8 * (e >> 2) + 4 * h + (e & 3) - j;
-          const bool in = (!a.causal || far >= 0) && (!a.window || (far < a.window && far > -a.window) || j < a.sinks);
-          x[e] = in ? x[e] : 0.0f;
-          y[e] = in ? y[e] : 0.0f;
+          const bool in = from + (uint32_t)(32 * b + 8 * (e >> 2) + (e & 3)) < span;
+          x[b][e] = in ? x[b][e] : 0.0f;
+          y[b][e] = in ? y[b][e] : 0.0f;
         }
-      }
+    }
+#pragma unroll
+    for (int b = 0; b < RBW; ++b) {
 #pragma unroll
       for (int i = 0; i < PSTEPS; ++i) {
-        const piece p = piece_of<D>(x, i);
+        const piece p = piece_of<D>(x[b], i);
 #pragma unroll
         for (int d = 0; d < NBO; ++d) dv[d] = mfma32<D>(T::transposed(gt, 32 * b + T::STEP * i, d0 + d, lane), p, dv[d]);
       }
-      scale.apply(y, dk);
+    }
+#pragma unroll
+    for (int b = 0; b < RBW; ++b) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[b][e] = x[b][e] * y[b][e];
+      scale.apply(y[b], dk);
 #pragma unroll
       for (int i = 0; i < PSTEPS; ++i) {
-        const piece p = piece_of<D>(y, i);
+        const piece p = piece_of<D>(y[b], i);
 #pragma unroll
         for (int d = 0; d < NBO; ++d) dk[d] = mfma32<D>(T::transposed(qt, 32 * b + T::STEP * i, d0 + d, lane), p, dk[d]);
       }
     }
   };
 
+  // Where the next tile to load lies, and the queries of it that exist.
   const uint32_t ldq = (uint32_t)(a.sq.t * T::ES), ldg = (uint32_t)(a.sdo.t * T::ES);
+  const int64_t nrows = all_rows(a);
   const char* qp = (const char*)a.q + base_of(a.sq, false, h0) * T::ES;
   const char* gp = (const char*)a.d_out + base_of(a.sdo, false, h0) * T::ES;
-  const float* const stats = a.stats + h0 * all_rows(a) + (a.q_starts ? s.q0 : s.b * a.q_tokens);
-  // Statistic w (0: of s, 1: of dP) of a tile's rows; rows past the last one have zeros, as their q and d_out.
-  auto stats_at = [&](int w, int g, int t) { return stats + (w * a.heads + g) * all_rows(a) + t; };
-  struct Place {
-    int g, t;
-  };
-  auto next = [&](Place& p) {
-    if (++p.g == a.group) {
-      p.g = 0;
-      p.t -= QT;
+  const float* sp = a.stats + h0 * nrows + (a.q_starts ? s.q0 : s.b * a.q_tokens);
+  const int64_t second_stats = a.heads * nrows;
+  // The tile in work, the next to load.
+  int t_here = t_lo + (per_head - 1 - i0 / a.group) * QT, g_here = i0 % a.group, t_next = t_here, g_next = g_here;
+  auto advance = [&](int& t, int& g) {
+    if (++g == a.group) {
+      g = 0;
+      t -= QT;
     }
   };
-  auto q_at = [&](const Place& p) { return qp + (p.t * a.sq.t + p.g * a.sq.h) * T::ES; };
-  auto g_at = [&](const Place& p) { return gp + (p.t * a.sdo.t + p.g * a.sdo.h) * T::ES; };
-  const int t_last = t_lo + (per_head - 1) * QT;
-  Place here{0, t_last}, ahead{0, t_last};  // the tile in work, and the next to load
+  auto q_at = [&]() { return qp + (t_next * a.sq.t + g_next * a.sq.h) * T::ES; };
+  auto g_at = [&]() { return gp + (t_next * a.sdo.t + g_next * a.sdo.h) * T::ES; };
+  auto s_at = [&]() { return sp + g_next * nrows + t_next; };
   if constexpr (ALN) {
     const uint32_t l0 = lds_offset(lds);
     S qs, gs;
     qs.init(ldq, a.dim, tid);
     gs.init(ldg, a.dim, tid);
-    const int w = min(wave, 2);  // waves 2 and 3 load nothing, so that all waves have as many loads in flight
-    constexpr int LOADS = 2 * S::NL + 1;
-    auto stage = [&](int buf, bool in) {
+    auto stage = [&](int buf) {
       const uint32_t to = l0 + buf * 2 * S::BYTES;
-      const int n = in ? t_end - ahead.t : 0;
-      qs.load(q_at(ahead), ldq, n, a.dim, to, wave);
-      gs.load(g_at(ahead), ldg, n, a.dim, to + S::BYTES, wave);
-      lds_load<4, false>(raw_desc(stats_at(w & 1, ahead.g, ahead.t), w < 2 && n > 0 ? 4 * min(n, QT) : 0), 4 * lane,
-                         __builtin_amdgcn_readfirstlane(lds_offset(&row_stats[buf][wave][0])));
-      if (in) next(ahead);
+      const int n = t_end - t_next;
+      qs.load(q_at(), ldq, n, a.dim, to, wave);
+      gs.load(g_at(), ldg, n, a.dim, to + S::BYTES, wave);
+      // Rows past the last one have zeros, as their q and d_out. 
+      if (wave < 2)
+        lds_load<4, false>(raw_desc(s_at() + (wave ? second_stats : 0)), lane < min(n, QT) ? 4 * lane : OUTSIDE,
+                           __builtin_amdgcn_readfirstlane(lds_offset(lds) + STATS + buf * 512 + wave * 256));
+      advance(t_next, g_next);
     };
-#pragma unroll
-    for (int i = 0; i < NST - 1; ++i) stage(i, i < count);
-    int buf = 0;
-    for (int i = 0; i < count; ++i) {
-      // Tile i has arrived; every wave is done with tile i - 1, whose buffer the next tile to load fills.
-      wait_loads<(NST - 2) * LOADS>();
+    if (count > 0) stage(0);
+    int i = 0;
+    auto step = [&](auto buffer) {
+      // Tile i has arrived; every wave is done with tile i - 1, whose buffer the next one fills.
+      wait_loads<0>();
       lds_barrier();
-      stage(buf == 0 ? NST - 1 : buf - 1, i + NST - 1 < count);
-      const unsigned char* cur = lds + buf * 2 * S::BYTES;
-      multiply(cur, cur + S::BYTES, buf, here.t);
-      next(here);
-      buf = buf == NST - 1 ? 0 : buf + 1;
+      if (++i < count) stage(1 - decltype(buffer)::value);
+      multiply(buffer, t_here);
+      advance(t_here, g_here);
+    };
+    // Two at a time, so that every LDS address is a lane's own plus a constant.
+    while (i < count) {
+      step(std::integral_constant<int, 0>());
+      if (i < count) step(std::integral_constant<int, 1>());
     }
-    wait_loads<0>();  // LDS must not be given up with loads into it in flight
   } else {
     uint4 fq[S::NL], fg[S::NL];
     float fs = 0.0f;
     auto fetch = [&]() {
-      S::fetch(q_at(ahead), ldq, t_end - ahead.t, a.dim, tid, fq);
-      S::fetch(g_at(ahead), ldg, t_end - ahead.t, a.dim, tid, fg);
-      fs = wave < 2 && lane < min(QT, t_end - ahead.t) ? stats_at(wave, ahead.g, ahead.t)[lane] : 0.0f;
-      next(ahead);
+      const int n = t_end - t_next;
+      S::fetch(q_at(), ldq, n, a.dim, tid, fq);
+      S::fetch(g_at(), ldg, n, a.dim, tid, fg);
+      fs = wave < 2 && lane < min(n, QT) ? s_at()[wave * second_stats + lane] : 0.0f;
+      advance(t_next, g_next);
     };
     if (count > 0) fetch();
     for (int i = 0; i < count; ++i) {
-      unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
-      S::put(cur, tid, fq);
-      S::put(cur + S::BYTES, tid, fg);
-      row_stats[i & 1][wave][lane] = fs;
+      lds_barrier();  // every wave is done with the tile before
+      S::put(lds, tid, fq);
+      S::put(lds + S::BYTES, tid, fg);
+      if (wave < 2) row_stats[0][wave][lane] = fs;
       lds_barrier();
       if (i + 1 < count) fetch();
-      multiply(cur, cur + S::BYTES, i & 1, here.t);
-      next(here);
+      multiply(std::integral_constant<int, 0>(), t_here);
+      advance(t_here, g_here);
     }
   }
   lds_barrier();
 
-  if constexpr (WR == 2) {
-    // The second share's sums to the first's, through LDS: 16 bytes of every lane at a time.
-    const float to_one = D == DT::F16 ? 1.0f / scale.by : 1.0f;  // each share has its own power of two
-    auto join = [&](f32x16 (&sum)[NBO], float f) {
-      f32x4* const at = (f32x4*)lds + (wk * NBO * 4) * 64 + lane;
-      if (wr == 1) {
+  unsigned char* const rows32 = lds + wave * 32 * T::RB;
+  auto write = [&](int second, void* to, const Strides3& st, const f32x16 (&sum)[NBO], float f) {
+    if (!to) return;
+    if (a.splits > 1) {
+      // fp32 parts [part][dv, dk][row of k][key head][dim]: four columns of a lane's key at a time.
+      const int64_t krows = a.k_starts ? a.k_tokens : a.batch * a.k_tokens;
+      float* const out = a.partial + (((part * 2 + second) * krows + (a.k_starts ? s.k0 : s.b * a.k_tokens) + j) * a.kv_heads + kvh) * a.dim;
+      if (j >= s.kl) return;
 #pragma unroll
-        for (int d = 0; d < NBO; ++d)
+      for (int d = 0; d < NBO; ++d)
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            at[(4 * d + u) * 64] = f32x4{sum[d][4 * u] * f, sum[d][4 * u + 1] * f, sum[d][4 * u + 2] * f, sum[d][4 * u + 3] * f};
-      }
-      lds_barrier();
-      if (wr == 0) {
+        for (int u = 0; u < 4; ++u) {
+          const int col = 32 * (d0 + d) + 8 * u + 4 * h;
+          const f32x4 v = {sum[d][4 * u] * f, sum[d][4 * u + 1] * f, sum[d][4 * u + 2] * f, sum[d][4 * u + 3] * f};
+          if (ALN) {  // dim is a multiple of four
+            if (col < a.dim) *(f32x4*)(out + col) = v;
+          } else {
 #pragma unroll
-        for (int d = 0; d < NBO; ++d)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const f32x4 v = at[(4 * d + u) * 64];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[d][4 * u + e] = sum[d][4 * u + e] * f + v[e];
+            for (int e = 0; e < 4; ++e)
+              if (col + e < a.dim) out[col + e] = v[e];
           }
-      }
-      lds_barrier();
-    };
-    join(dv, 1.0f);
-    join(dk, to_one);
-    if (wr != 0) return;
-  }
-  unsigned char* const rows32 = lds + wk * 32 * T::RB;
-  auto write = [&](void* base, const Strides3& st, const f32x16 (&sum)[NBO], float f) {
-    if (!base) return;
+        }
+      return;
+    }
     rows_to_lds<D, NB>(rows32, sum, f, lane);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     constexpr int CPR = 32 * NBO / T::EPC;
+    char* const base = (char*)to + base_of(st, true, kvh) * T::ES;
 #pragma unroll 4
     for (int i = lane; i < 32 * CPR; i += 64) {
-      const int row = i / CPR, ch = i % CPR;
-      if (jw + row >= s.kl) continue;
-      char* to = (char*)base + (base_of(st, true, kvh) + (jw + row) * st.t) * T::ES;
-      put_chunk16<D, ALN>(to, 32 * d0 + ch * T::EPC, a.dim, row_chunk<D, NB>(rows32, row, ch));
+      const int row = jw + i / CPR, ch = i % CPR;
+      if (row < s.kl)
+        put_chunk16<D, ALN>(base + row * st.t * T::ES, 32 * d0 + ch * T::EPC, a.dim, row_chunk<D, NB>(rows32, i / CPR, ch));
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
-  write(a.dv, a.sdv, dv, D == DT::F16 ? 0x1p-15f : 1.0f);
-  write(a.dk, a.sdk, dk, (D == DT::F16 ? 0x1p-15f : 1.0f) * (WR == 2 ? a.scale : a.scale * scale.undo()));
+  // fp16: the weights' 2^15 taken back, and the columns' power of two.
+  constexpr float DOWN = D == DT::F16 ? 0x1p-15f : 1.0f;
+  write(0, a.dv, a.sdv, dv, DOWN);
+  write(1, a.dk, a.sdk, dk, DOWN * a.scale * scale.undo());
+}
+
+// The parts of dv and dk added in ascending order, for the rows of k that belong to sequences. One thread per four elements
+// where dim is a multiple of four, else per element.
+template <DT D, int V> __global__ __launch_bounds__(256) void k_attention_join(const AttnArgs a) {
+  const int64_t krows = a.k_starts ? a.k_tokens : a.batch * a.k_tokens, per = (int64_t)a.kv_heads * a.dim, all = krows * per;
+  int64_t r0 = 0, r1 = krows;
+  if (a.k_starts) {
+    r0 = min(max((int64_t)a.k_starts[0], (int64_t)0), krows);
+    r1 = min(max((int64_t)a.k_starts[a.batch], r0), krows);
+  }
+  const bool second = blockIdx.y;
+  void* const to = second ? a.dk : a.dv;
+  const Strides3 st = second ? a.sdk : a.sdv;
+  if (!to) return;
+  for (int64_t i = r0 * per + ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; i < r1 * per; i += (int64_t)gridDim.x * 256 * V) {
+    float x[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = 0.0f;
+    for (int p = 0; p < a.splits; ++p) {
+      const float* const from = a.partial + (p * 2 + second) * all + i;
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] = x[e] + from[e];
+    }
+    const int64_t row = i / per;
+    const int c = (int)(i - row * per), head = c / a.dim, col = c - head * a.dim;
+    const int64_t b = a.k_starts ? 0 : row / a.k_tokens;
+    const int64_t at = b * st.b + (row - b * a.k_tokens) * st.t + head * st.h + col;
+#pragma unroll
+    for (int e = 0; e < V; ++e) hc::st<D>(to, at + e, x[e]);
+  }
 }
 
 namespace {
+
+// Parts that the rows are split into: enough workgroups for three on every compute unit, no part of fewer than 16 tiles of 32
+// rows. 2 x 4096 tokens with 20/4 heads of 128 (256 tiles of keys): in one part 1890 us, in two 762, in three 704, in four
+// 755, the sums' join (134 MB a part) included.
+constexpr int64_t MOST_PARTS = 4, ENOUGH = 768;
+template <DT D, int NB> int dkv_parts(const AttnArgs& a) {
+  const int64_t krows = a.k_starts ? a.k_tokens : a.batch * a.k_tokens, tk = DkvShape<D, NB>::TK;
+  const int64_t groups = std::max<int64_t>((krows + tk - 1) / tk, a.k_starts ? 1 : a.batch) * a.kv_heads * DkvShape<D, NB>::HALVES;
+  const int64_t rows = a.q_tokens * a.group / (a.k_starts ? a.batch : 1);
+  return (int)std::max<int64_t>(1, std::min({MOST_PARTS, (ENOUGH + groups - 1) / groups, rows / (16 * 32)}));
+}
 
 template <DT D, int NB> hipError_t go(const AttnArgs& a0, bool aligned, hipStream_t s) {
   AttnArgs a = a0;
@@ -488,17 +550,18 @@ template <DT D, int NB> hipError_t go(const AttnArgs& a0, bool aligned, hipStrea
     else hipLaunchKernelGGL((k_attention_dq<D, NB, false>), grid, block, 0, s, a);
   }
   if ((a.dk || a.dv) && a.k_tokens > 0) {
-    auto run = [&](auto wk) {
-      constexpr int WK = decltype(wk)::value;
-      typedef DkvShape<D, NB, WK> F;
-      const int64_t n = tiles(a.k_starts, a.k_tokens, F::TK);
-      const dim3 grid((unsigned)(n * a.kv_heads * F::HALVES)), block(256);
-      if (aligned) hipLaunchKernelGGL((k_attention_dkv<D, NB, WK, true>), grid, block, 0, s, a);
-      else hipLaunchKernelGGL((k_attention_dkv<D, NB, WK, false>), grid, block, 0, s, a);
-    };
-    if constexpr (Rows<D, NB>::RB >= 1024) run(std::integral_constant<int, 4>());
-    else if (getenv("WK4")) run(std::integral_constant<int, 4>());
-    else run(std::integral_constant<int, 2>());
+    const int64_t n = tiles(a.k_starts, a.k_tokens, DkvShape<D, NB>::TK);
+    a.splits = dkv_parts<D, NB>(a);
+    const dim3 grid((unsigned)(n * a.kv_heads * a.splits * DkvShape<D, NB>::HALVES)), block(256);
+    if (aligned) hipLaunchKernelGGL((k_attention_dkv<D, NB, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_attention_dkv<D, NB, false>), grid, block, 0, s, a);
+    if (a.splits > 1) {
+      const int64_t krows = a.k_starts ? a.k_tokens : a.batch * a.k_tokens, all = krows * a.kv_heads * a.dim;
+      const int v = a.dim % 4 == 0 ? 4 : 1;
+      const dim3 g2((unsigned)std::min<int64_t>((all / v + 255) / 256, 8192), 2);
+      if (v == 4) hipLaunchKernelGGL((k_attention_join<D, 4>), g2, block, 0, s, a);
+      else hipLaunchKernelGGL((k_attention_join<D, 1>), g2, block, 0, s, a);
+    }
   }
   return hipGetLastError();
 }
@@ -511,7 +574,13 @@ template <DT D> hipError_t go_dim(const AttnArgs& a, bool aligned, hipStream_t s
 
 }  // namespace
 
+// Bytes of the rows' statistics.
+static size_t stats_bytes(const AttnArgs& a) {
+  return ((size_t)(a.q_starts ? a.q_tokens : a.batch * a.q_tokens) * a.heads * 2 * sizeof(float) + 255) & ~(size_t)255;
+}
+
 hipError_t launch_attention_backward(AttnArgs a, int dtype, bool aligned, hipStream_t s) {
+  a.partial = (float*)((char*)a.stats + stats_bytes(a));
   switch (dtype) {
     case (int)DT::F32: return go_dim<DT::F32>(a, aligned, s);
     case (int)DT::F16: return go_dim<DT::F16>(a, aligned, s);
@@ -519,8 +588,10 @@ hipError_t launch_attention_backward(AttnArgs a, int dtype, bool aligned, hipStr
   }
 }
 
+// The rows' statistics, then the parts' sums: at most parts of ENOUGH workgroups' keys beside one of all keys.
 size_t attention_backward_scratch(const AttnArgs& a, int) {
-  return (size_t)(a.q_starts ? a.q_tokens : a.batch * a.q_tokens) * a.heads * 2 * sizeof(float);
+  const int64_t n = a.q_starts ? 1 : a.batch, keys = n * a.k_tokens * a.kv_heads;
+  return stats_bytes(a) + (size_t)std::min(MOST_PARTS * keys, ENOUGH * 128 + keys) * a.dim * 2 * sizeof(float);
 }
 
 }  // namespace hc
