@@ -373,12 +373,8 @@ def page_map(cached, fresh, block_table, free_pages, *, page_size: int, tokens: 
     sizes = (batch + 1, batch, tokens, tokens, batch + 1)
     if out is None:
         # one allocation, each part on 16 bytes
-        first, parts = 0, []
-        for n in sizes:
-            parts.append(first)
-            first += (n + 3) & ~3
-        whole = torch.empty(first, dtype=torch.int32, device=cached.device)
-        out = [whole[i:i + n] for i, n in zip(parts, sizes)]
+        whole = torch.empty(sum((n + 3) & ~3 for n in sizes), dtype=torch.int32, device=cached.device)
+        out = [x[:n] for x, n in zip(whole.split_with_sizes([(n + 3) & ~3 for n in sizes]), sizes)]
     else:
         for t, n, name in zip(out, sizes, ("starts", "lengths", "positions", "slots", "taken")):
             _ints(t, cached, (n,), name)

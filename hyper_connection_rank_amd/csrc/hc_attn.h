@@ -52,6 +52,7 @@ struct PagedArgs {
   int64_t table_stride;
   int64_t pages;
   int page, most_pages;   // rows of a page; entries of a sequence in the table
+  int page_shift;         // log2 of page, or -1
   int batch, heads, kv_heads, group, dim;
   int window, sinks;
   float scale;
@@ -295,6 +296,11 @@ __device__ __forceinline__ float halves_sum(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
+
+// fp16 weights are taken 2^7 times as large, so that fewer of them fall below fp16's normal numbers; with the maximum up
+// to 2^8 behind (see below) they reach 2^15.
+template <DT D> constexpr float weight_shift() { return D == DT::F16 ? 7.0f : 0.0f; }
+constexpr float LAG = 8.0f;
 
 // Which keys a query sees: j with lo <= j <= hi or j < first.
 struct Sees {

@@ -21,11 +21,6 @@ template <DT D, int NB> struct FwdShape {
   static constexpr int WAVES = 4, QB = 1, TR = 32 * QB * WAVES;
 };
 
-// fp16 weights are taken 2^7 times as large, so that fewer of them fall below fp16's normal numbers; with the maximum up
-// to 2^8 behind (see below) they reach 2^15.
-template <DT D> constexpr float weight_shift() { return D == DT::F16 ? 7.0f : 0.0f; }
-constexpr float LAG = 8.0f;
-
 template <DT D, int NB, bool ALN>
 __global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? 2 : 1)) void k_attention(const AttnArgs a) {
   typedef FwdShape<D, NB> F;

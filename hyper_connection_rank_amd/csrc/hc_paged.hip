@@ -11,15 +11,19 @@ namespace hc {
 
 // A workgroup takes one sequence, one key head with up to 16 of the query heads that share it, and a part of the
 // sequence's keys; its waves take tiles of keys in turn, each through buffers of its own, so no wave waits for
-// another before the end. As in hc_attn.hip the products are transposed (16 x 16 results here: few rows).
-// The cache's rows are read once, by loads that write LDS directly; they bound the kernel.
+// another before the end. As in hc_attn.hip the products are transposed (16 x 16 results here: few rows). A lane looks
+// after one key of every block of 16: it finds the key's page, loads 16 bytes in every 64 of the key's row of k, as
+// the matrix op wants them, and of its row of v, which goes to LDS directly to be read transposed. The cache's
+// rows are read once; they bound the kernel, so two tiles of every wave are on their way or in work at all times.
+
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
 
 template <DT D, int NB> struct PagedShape {
   typedef Rows<D, NB> T;
-  static constexpr int KT = T::RB <= 128 ? 64 : T::RB >= 1024 && D == DT::F32 ? 16 : 32;  // keys of a tile
-  static constexpr int TILE = KT * T::RB;
-  static constexpr int RING = 4 * TILE;  // bytes of a wave: two buffers of K and V
-  static constexpr int WAVES = RING * 4 <= 131072 ? 4 : 2;
+  static constexpr int KT = D == DT::F32 ? 16 : 32;  // keys of a tile
+  static constexpr int TILE = KT * T::RB;            // bytes of a tile of v
+  static constexpr int RING = 2 * TILE, WAVES = 4;
+
 };
 
 struct PagedSeq {
@@ -62,27 +66,30 @@ __device__ __forceinline__ float* part_sums(const PagedArgs& a, int64_t head, in
 }
 
 template <DT D, int NB, bool ALN>
-__global__ __launch_bounds__((64 * PagedShape<D, NB>::WAVES)) void k_paged(const PagedArgs a) {
+__global__ __launch_bounds__(256, (ALN && NB <= 4 ? 2 : 1)) void k_paged(const PagedArgs a) {
   typedef PagedShape<D, NB> F;
   typedef Rows<D, NB> T;
   typedef typename T::piece piece;
   constexpr int KT = F::KT, WAVES = F::WAVES, KB = KT / 16;
-  constexpr int STEP = D == DT::F32 ? 16 : 32, STEPS = 32 * NB / STEP;  // contraction of a score
-  constexpr int DB = 2 * NB;                                           // blocks of 16 columns
-  constexpr int NL = F::TILE / 1024;                                   // loads that fill a tile
+  constexpr int STEPS = T::CPR / 4;  // loads of a row: 16 bytes in every 64; the contraction of a score in as many steps
+  constexpr int DB = 2 * NB;         // blocks of 16 columns
   static_assert(16 * 32 * NB * 4 <= F::RING, "a wave's sums fit its buffers");
   __shared__ __attribute__((aligned(1024))) unsigned char lds[WAVES * F::RING];
   __shared__ float stat[WAVES][2][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4;
 
-  // Parts fastest, so that a sequence's parts are in flight together.
+  // Parts slowest: workgroups go to the XCDs in turn, and short sequences have only the first parts, which would all be on
+  // the same few (64 sequences of 1 to 16384 keys: 322 us with parts fastest).
   const int blocks = (a.group + 15) / 16;  // of rows
-  int id = blockIdx.x;
-  const int part = id % a.splits;
-  id /= a.splits;
+  const int pairs = a.batch * a.kv_heads * blocks;
+  const int part = blockIdx.x / pairs;
+  int id = blockIdx.x - part * pairs;
+  // Heads turn with every eight workgroups, so that an XCD does not read one head's columns alone, which would all be
+  // in the same few channels of its L2 (the same case with 4 heads of 128: 255 us without, 228 with).
   const int rb = id % blocks;
   id /= blocks;
-  const int kvh = id % a.kv_heads, b = id / a.kv_heads;
+  const int b = id / a.kv_heads, turn = b * a.kv_heads * blocks / 8 + part;  // the same for all heads of a sequence's part
+  const int kvh = (id - b * a.kv_heads + turn) % a.kv_heads;
   const PagedSeq s = paged_seq<KT>(a, b);
   if (part >= s.parts) return;
   const int t0 = part * s.per, t1 = min(t0 + s.per, s.count);
@@ -102,90 +109,116 @@ __global__ __launch_bounds__((64 * PagedShape<D, NB>::WAVES)) void k_paged(const
   const float c = a.scale * LOG2E;
   unsigned char* const ring = lds + wave * F::RING;
 
-  // Lane l looks after key l % KT of a tile: the page that holds it, one tile ahead of its loads.
+  // The pages of this lane's keys of a tile, and its rows' offsets there: -1 where the key is not seen, or on a page that
+  // the cache does not have.
   const int* table = a.table + (int64_t)b * a.table_stride;
-  auto page_of = [&](int i) {
-    const int j = s.tile(min(i, s.count - 1)) * KT + (lane & (KT - 1));
-    return j < s.len ? table[j / a.page] : -1;
+  struct Keys {
+    int page[KB];
+    int64_t at[KB];
   };
-  // Its row's offset in the caches, or -1: not seen, or on a page that the cache does not have.
-  auto offset_of = [&](int i, int page) {
-    const int j = s.tile(i) * KT + (lane & (KT - 1));
-    const bool in = j < s.len && (j >= s.lo || j < s.first) && page >= 0 && page < a.pages;
-    return in ? (int64_t)page * a.sc.b + (int64_t)(j % a.page) * a.sc.t + (int64_t)kvh * a.sc.h : (int64_t)-1;
-  };
-  auto stage = [&](int64_t at, unsigned char* to) {
+  const int shift = a.page_shift;
+  auto key_of = [&](int i, int k) { return s.tile(i) * KT + 16 * k + (lane & 15); };
+  auto find_pages = [&](int i, Keys& x) {
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int row = (i * 64 + lane) / T::CPR, col = ((lane % T::CPR) ^ T::swz(row)) * T::EPC;
-      const uint32_t lo = __shfl((uint32_t)at, row, 64), hi = __shfl((uint32_t)((uint64_t)at >> 32), row, 64);
-      const int64_t from = (int64_t)((uint64_t)hi << 32 | lo);
-      if constexpr (ALN) {
-        const bool in = from >= 0 && col < a.dim;
-        const char* kp = in ? (const char*)a.k + (from + col) * T::ES : (const char*)zeros16;
-        const char* vp = in ? (const char*)a.v + (from + col) * T::ES : (const char*)zeros16;
-        const uint32_t dst = __builtin_amdgcn_readfirstlane(lds_offset(to) + i * 1024);
-        lds_load_from(kp, dst);
-        lds_load_from(vp, dst + F::TILE);
-      } else {
-        uint4 kv = make_uint4(0u, 0u, 0u, 0u), vv = kv;
-        if (from >= 0) {
-          kv = chunk16<D, false>((const char*)a.k + from * T::ES, col, a.dim);
-          vv = chunk16<D, false>((const char*)a.v + from * T::ES, col, a.dim);
-        }
-        *(uint4*)(to + i * 1024 + lane * 16) = kv;
-        *(uint4*)(to + F::TILE + i * 1024 + lane * 16) = vv;
-      }
+    for (int k = 0; k < KB; ++k) {
+      const int j = key_of(i, k);
+      x.page[k] = i < t1 && j < s.len ? table[shift >= 0 ? j >> shift : j / a.page] : -1;
     }
   };
+  auto find_rows = [&](int i, Keys& x) {
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int j = key_of(i, k), r = shift >= 0 ? j & (a.page - 1) : j % a.page;
+      const bool in = j < s.len && (j >= s.lo || j < s.first) && x.page[k] >= 0 && x.page[k] < a.pages;
+      x.at[k] = in ? ((int64_t)x.page[k] * a.sc.b + (int64_t)r * a.sc.t + (int64_t)kvh * a.sc.h) * T::ES : (int64_t)-1;
+    }
+  };
+  // v in LDS: [block of 16 keys][chunk of 16 bytes][key]; one load fills four chunks of a block.
+  uint4 kn[KB][STEPS], vn[ALN ? 1 : KB][ALN ? 1 : STEPS];
+  auto load = [&](const Keys& x, unsigned char* to) {
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int col = (4 * i + g) * T::EPC;
+        if constexpr (ALN) {
+          const bool in = x.at[k] >= 0 && col < a.dim;
+          kn[k][i] = *(const uint4*)(in ? (const char*)a.k + x.at[k] + col * T::ES : (const char*)zeros16);
+          lds_load_from(in ? (const char*)a.v + x.at[k] + col * T::ES : (const char*)zeros16,
+                        __builtin_amdgcn_readfirstlane(lds_offset(to) + (k * STEPS + i) * 1024));
+        } else {
+          kn[k][i] = vn[k][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (x.at[k] >= 0) {
+            kn[k][i] = chunk16<D, false>((const char*)a.k + x.at[k], col, a.dim);
+            vn[k][i] = chunk16<D, false>((const char*)a.v + x.at[k], col, a.dim);
+          }
+        }
+      }
+  };
+  auto chunk_at = [](int k, int ch, int key) { return ((k * T::CPR + ch) * 16 + key) * 16; };
 
   int buf = 0, i = t0 + wave;
-  int64_t at = -1, next = -1;
-  int page = 0;
+  Keys now, next;
   if (i < t1) {
-    at = offset_of(i, page_of(i));
-    stage(at, ring);
-    page = page_of(i + WAVES);
+    find_pages(i, now);
+    find_rows(i, now);
+    load(now, ring);
+    find_pages(i + WAVES, next);
   }
   for (; i < t1; i += WAVES, buf ^= 1) {
     // Tile i has arrived (and the pages of the next); the reads of the tile before it are done.
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    const bool more = i + WAVES < t1;
-    if (more) {
-      next = offset_of(i + WAVES, page);
-      stage(next, ring + (buf ^ 1) * 2 * F::TILE);
-      page = page_of(i + 2 * WAVES);
+    piece kc[KB][STEPS];
+    bool seen[KB];
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      seen[k] = now.at[k] >= 0;
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) kc[k][st] = __builtin_bit_cast(piece, kn[k][st]);
     }
-    const unsigned char* kt = ring + buf * 2 * F::TILE;
-    const unsigned char* vt = kt + F::TILE;
-    const uint64_t seen = __ballot(at >= 0);  // bit j: key j of the tile
+    const unsigned char* vt = ring + buf * F::TILE;
+    if constexpr (!ALN) {
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) *(uint4*)(ring + buf * F::TILE + (k * STEPS + st) * 1024 + lane * 16) = vn[k][st];
+    }
+    if (i + WAVES < t1) {
+      now = next;
+      find_rows(i + WAVES, now);
+      load(now, ring + (buf ^ 1) * F::TILE);
+      find_pages(i + 2 * WAVES, next);
+    }
     f32x4 x[KB];
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
       x[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
-        const int row = 16 * k + (lane & 15);
-        const piece f = __builtin_bit_cast(piece, *(const uint4*)(kt + row * T::RB + (((4 * st + g) ^ T::swz(row)) << 4)));
         if constexpr (D == DT::F32) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[k] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[e], q[st][e], x[k], 0, 0, 0);
+          for (int e = 0; e < 4; ++e) x[k] = __builtin_amdgcn_mfma_f32_16x16x4f32(kc[k][st][e], q[st][e], x[k], 0, 0, 0);
         } else {
-          x[k] = mfma<D>(f, q[st], x[k]);
+          x[k] = mfma<D>(kc[k][st], q[st], x[k]);
         }
       }
     }
     float top = NEG_INF;
 #pragma unroll
-    for (int k = 0; k < KB; ++k)
+    for (int k = 0; k < KB; ++k) {
+      const uint64_t bits = __ballot(seen[k]);  // bit j: key j of the block
+      if (bits != ~0ull) {
+        const uint32_t mine = (uint32_t)bits >> (4 * g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[k][e] = (seen >> (16 * k + 4 * g + e)) & 1 ? x[k][e] : NEG_INF;
-        top = fmaxf(top, x[k][e]);
+        for (int e = 0; e < 4; ++e) x[k][e] = (mine >> e) & 1 ? x[k][e] : NEG_INF;
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, x[k][e]);
+    }
     top = quarters_max(top) * c;
-    const float grown = fmaxf(m, top);
-    if (__ballot(grown > m)) {
+    // As in hc_attn.hip: sums are scaled down only when the maximum has grown by more than 2^LAG since.
+    if (__ballot(top > m + LAG)) {
+      const float grown = fmaxf(m, top);
       const float f = grown == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(m - grown);
       m = grown;
       l *= f;
@@ -194,8 +227,7 @@ __global__ __launch_bounds__((64 * PagedShape<D, NB>::WAVES)) void k_paged(const
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[d][e] *= f;
     }
-    // fp16 weights 2^15 times as large: fewer fall below fp16's normal numbers.
-    const float base = (D == DT::F16 ? 15.0f : 0.0f) - (m == NEG_INF ? 0.0f : m);
+    const float base = weight_shift<D>() - (m == NEG_INF ? 0.0f : m);
 #pragma unroll
     for (int k = 0; k < KB; ++k)
 #pragma unroll
@@ -210,28 +242,22 @@ __global__ __launch_bounds__((64 * PagedShape<D, NB>::WAVES)) void k_paged(const
         for (int d = 0; d < DB; ++d)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int row = 16 * k + 4 * g + e, ch = 4 * d + ((lane & 15) >> 2);
-            const float f = *(const float*)(vt + row * T::RB + ((ch ^ T::swz(row)) << 4) + 4 * (lane & 3));
+            const float f = *(const float*)(vt + chunk_at(k, 4 * d + ((lane & 15) >> 2), 4 * g + e) + 4 * (lane & 3));
             o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(f, x[k][e], o[d], 0, 0, 0);
           }
     } else {
 #pragma unroll
-      for (int k = 0; k < KB; k += 2) {  // contraction over 32 keys: this lane's are 16 k + 4 g .. + 3 and 16 keys further
-        const u32x4 w = {pack2<D>(x[k][0], x[k][1]), pack2<D>(x[k][2], x[k][3]), pack2<D>(x[k + 1][0], x[k + 1][1]),
-                         pack2<D>(x[k + 1][2], x[k + 1][3])};
-        const s16x8 p = __builtin_bit_cast(s16x8, w);
+      for (int k = 0; k < KB; ++k) {  // this lane's keys are 16 k + 4 g .. + 3
+        const s16x4 p = __builtin_bit_cast(s16x4, u32x2{pack2<D>(x[k][0], x[k][1]), pack2<D>(x[k][2], x[k][3])});
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
-          const int j = lane & 15, row = 16 * k + 4 * g + (j >> 2), ch = 2 * d + ((j & 3) >> 1);
-          lds_u8* v0 = (lds_u8*)(vt + row * T::RB + ((ch ^ T::swz(row)) << 4) + 8 * (j & 1));
-          lds_u8* v1 = v0 + 16 * T::RB;  // the permutation repeats every 16 rows
-          const s16x4 f0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v0);
-          const s16x4 f1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v1);
-          o[d] = mfma<D>(__builtin_shufflevector(f0, f1, 0, 1, 2, 3, 4, 5, 6, 7), p, o[d]);
+          const int j = lane & 15, key = 4 * g + (j >> 2), ch = 2 * d + ((j & 3) >> 1);
+          const s16x4 f = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_u8*)(vt + chunk_at(k, ch, key) + 8 * (j & 1)));
+          if constexpr (D == DT::BF16) o[d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(f, p, o[d], 0, 0, 0);
+          else o[d] = __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4_t, f), __builtin_bit_cast(f16x4_t, p), o[d], 0, 0, 0);
         }
       }
     }
-    at = next;
   }
 
   // The waves' results joined in their order: sums of each row in LDS [row][32 NB], in this wave's own buffers.
@@ -279,20 +305,43 @@ template <DT D, int KT> __global__ __launch_bounds__(256) void k_paged_join(cons
   const PagedSeq s = paged_seq<KT>(a, b);
   if (s.parts == 1) return;
   const int used = (s.count + s.per - 1) / s.per;  // parts that hold tiles
-  // Wave w takes the parts w, w + 4, ...; the maximum first.
+  // The parts' weights, one lane for each (two rounds: up to 128 parts), then wave w adds parts w, w + 4, ..., eight loads at
+  // a time.
+  float pm[2], ps[2];
   float top = NEG_INF;
-  for (int p = lane; p < used; p += 64) top = fmaxf(top, part_sums(a, head, p)[0]);
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int p = lane + 64 * r;
+    pm[r] = p < used ? part_sums(a, head, p)[0] : NEG_INF;
+    ps[r] = p < used ? part_sums(a, head, p)[1] : 0.0f;
+    top = fmaxf(top, pm[r]);
+  }
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-  float sum = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int p = wave; p < used; p += 4) {
-    const float pm = part_sums(a, head, p)[0];
-    const float f = pm == NEG_INF ? 0.0f : __builtin_amdgcn_exp2f(pm - top);
-    sum = sum + f * part_sums(a, head, p)[1];
-    const float* v = part_values(a, head, p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 64 * i < a.dim) y[i] = y[i] + f * v[lane + 64 * i];
+  for (int r = 0; r < 2; ++r) {
+    pm[r] = pm[r] == NEG_INF ? 0.0f : __builtin_amdgcn_exp2f(pm[r] - top);
+    ps[r] = ps[r] * pm[r];
+  }
+  float sum = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int p0 = wave; p0 < used; p0 += 32) {
+    float v[8][4];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float* from = part_values(a, head, min(p0 + 4 * u, used - 1));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[u][i] = lane + 64 * i < a.dim ? from[lane + 64 * i] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int p = p0 + 4 * u;
+      if (p < used) {
+        const float f = __shfl(p < 64 ? pm[0] : pm[1], p & 63, 64);
+        sum = sum + __shfl(p < 64 ? ps[0] : ps[1], p & 63, 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = y[i] + f * v[u][i];
+      }
+    }
   }
   if (lane == 0) sum4[wave] = sum;
 #pragma unroll
@@ -314,11 +363,12 @@ template <DT D, int NB> void plan(PagedArgs& a) {
   const int64_t most = std::max<int64_t>((int64_t)a.most_pages * a.page, 1);  // keys
   const int64_t pairs = (int64_t)a.batch * a.kv_heads * ((a.group + 15) / 16);
   const int64_t least = 2 * F::KT * F::WAVES;
-  int64_t chunk = most * pairs / 1024;
+  int64_t chunk = most * pairs / 512;
   chunk = std::min<int64_t>(std::max(chunk, least), 1024);
   chunk = (chunk + F::KT - 1) / F::KT * F::KT;
   a.chunk = (int)chunk;
   // A launch holds 2^24 workgroups of 256 threads.
+  a.page_shift = (a.page & (a.page - 1)) == 0 ? __builtin_ctz(a.page) : -1;
   a.splits = (int)std::min<int64_t>(std::min<int64_t>((most + chunk - 1) / chunk, 128), std::max<int64_t>((1 << 23) / pairs, 1));
 }
 
@@ -525,11 +575,43 @@ __device__ __forceinline__ void fill_maps(const MapArgs& a, const int* starts, c
 
 __global__ __launch_bounds__(256) void k_page_fill(const MapArgs a) { fill_maps(a, a.starts, a.taken); }
 
+// Up to 1024 requests in one launch: every workgroup takes the sums for itself, in LDS, and the first one writes them.
+__global__ __launch_bounds__(MAP_THREADS) void k_page_map(const MapArgs a) {
+  __shared__ int64_t part[MAP_THREADS / 64][2];
+  __shared__ int starts[MAP_THREADS + 1], taken[MAP_THREADS + 1];
+  const int tid = threadIdx.x;
+  int64_t x = 0, y = 0;
+  Request r{};
+  if (tid < a.batch) {
+    r = request(a, tid);
+    x = r.fresh;
+    y = r.missing;
+  }
+  group_scan(x, y, part, tid);
+  if (tid == 0) starts[0] = taken[0] = 0;
+  starts[tid + 1] = to_int(x);
+  taken[tid + 1] = to_int(y);
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    if (tid < a.batch) {
+      a.lengths[tid] = to_int(r.cached + r.fresh);
+      a.starts[tid + 1] = starts[tid + 1];
+      a.taken[tid + 1] = taken[tid + 1];
+    }
+    if (tid == 0) a.starts[0] = a.taken[0] = 0;
+  }
+  fill_maps(a, starts, taken);
+}
+
+// One launch up to 1024 requests (64 requests of one token 6.6 us in two kernels, 4 in one).
 hipError_t launch_page_map(const MapArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(k_page_sums, dim3(1), dim3(MAP_THREADS), 0, s, a);
   const int64_t n = std::max<int64_t>(a.tokens, a.batch);
-  if (a.batch > 0 || a.tokens > 0)
-    hipLaunchKernelGGL(k_page_fill, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 2048)), dim3(256), 0, s, a);
+  if (a.batch <= MAP_THREADS) {
+    hipLaunchKernelGGL(k_page_map, dim3((unsigned)std::min<int64_t>(std::max<int64_t>((n + MAP_THREADS - 1) / MAP_THREADS, 1), 256)), dim3(MAP_THREADS), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(k_page_sums, dim3(1), dim3(MAP_THREADS), 0, s, a);
+  hipLaunchKernelGGL(k_page_fill, dim3((unsigned)std::min<int64_t>((n + 255) / 256, 2048)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
