@@ -13,6 +13,9 @@ U, F and ``within`` as in ``_ffn``. The bounds add up, for one query:
    numbers half a step is 2^-25, 2^-32 (2^-40) of the largest weight.
  - dS rounded to T likewise; in fp16 scaled so that a column's largest value
    so far is at least 2^11: half a step is 2^-36 of it.
+ - the hardware's exponential has no subnormal results, nor have the matrix
+   units subnormal operands: a weight or dS below 2^-126 may count as 0, an
+   absolute error of at most 2^-126 each, LEAST = 2^-125 for both.
  - fp32 sums over n keys (or rows): 8 F sqrt(n) (norm2(terms) + |sum|), and a
    few rescalings of the sums, 64 F sum|terms|.
 """
@@ -23,6 +26,8 @@ import math
 import torch
 
 from _ffn import F, U
+
+LEAST = 2.0 ** -125
 
 
 def visible(ql, kl, causal, window, sinks, device="cuda"):
@@ -60,7 +65,7 @@ def head(q, k, v, see, scale, dt):
     cnt = max(s.shape[1], 1)
     pv = torch.sqrt((p * p) @ (v * v))
     bound = (p * e) @ v.abs() + (p * e).sum(1, keepdim=True) * o.abs()
-    bound = bound + 8 * F * math.sqrt(cnt) * (pv + 2 * o.abs()) + 64 * F * (p @ v.abs())
+    bound = bound + 8 * F * math.sqrt(cnt) * (pv + 2 * o.abs()) + 64 * F * (p @ v.abs()) + LEAST * (see.double() @ v.abs())
     if dt != torch.float32:
         bound = bound + 4 * U(dt) * pv
     if dt == torch.float16:
@@ -84,7 +89,8 @@ def head_backward(q, k, v, out, lse, do, see, scale, dt):
     edl = 8 * F * r * (torch.sqrt((out * out * do * do).sum(1, keepdim=True)) + delta.abs())
     t = dp - delta
     ds = p * t
-    eds = p * (e * t.abs() + edp + edl + 4 * F * (dp.abs() + delta.abs()))
+    seen = see.double()
+    eds = p * (e * t.abs() + edp + edl + 4 * F * (dp.abs() + delta.abs())) + LEAST * seen * (1 + t.abs())
     low = dt != torch.float32
 
     def total(a, ea, b, small):
@@ -103,7 +109,7 @@ def head_backward(q, k, v, out, lse, do, see, scale, dt):
 
     dq, bq = total(ds.t(), eds.t(), k, top(ds.t()))
     dk, bk = total(ds, eds, q, top(ds))
-    dv, bv = total(p, p * e, do, 2.0 ** -40)
+    dv, bv = total(p, p * e + LEAST * seen, do, 2.0 ** -40)
     return {"dq": (scale * dq, scale * bq), "dk": (scale * dk, scale * bk), "dv": (dv, bv)}
 
 
