@@ -38,7 +38,7 @@ def _strides(*names):
 class AttentionProblem(ctypes.Structure):
     _fields_ = [("batch", _I64), ("q_tokens", _I64), ("k_tokens", _I64), ("heads", _I32), ("kv_heads", _I32), ("dim", _I32),
                 ("dtype", _I32), ("causal", _I32), ("window", _I32), ("sinks", _I32), ("packed", _I32), ("scale", _F32),
-                ("reserved", _I32 * 2)] + _strides("q", "k", "v", "out", "d_out", "dq", "dk", "dv", "lse")
+                ("zero_rest", _I32), ("reserved", _I32)] + _strides("q", "k", "v", "out", "d_out", "dq", "dk", "dv", "lse")
 
 
 class PagedProblem(ctypes.Structure):
@@ -182,7 +182,7 @@ def _whole(q, k, v, causal, window, sinks, scale, q_starts, k_starts):
             _refuse("k_starts may be left out only where q and k have the same rows")
     st = _rows(q, q, q.shape, "q") + _rows(k, q, shape, "k") + _rows(v, q, shape, "v")
     return (batch, q.shape[-3], k_tokens, heads, kv_heads, dim, code, 1 if causal else 0, _count(window, "window"),
-            _count(sinks, "sinks"), 1 if packed else 0, _scale_of(scale, dim), (_I32 * 2)()), st
+            _count(sinks, "sinks"), 1 if packed else 0, _scale_of(scale, dim)), st
 
 
 def attention(q, k, v, *, causal=True, window=0, sinks=0, scale=None, q_starts=None, k_starts=None, save=False, out=None,
@@ -207,11 +207,13 @@ def attention(q, k, v, *, causal=True, window=0, sinks=0, scale=None, q_starts=N
     """
     _unrecorded(q, k, v)
     fields, st = _whole(q, k, v, causal, window, sinks, scale, q_starts, k_starts)
-    new = torch.empty if q_starts is None else torch.zeros
-    if out is None:
-        out = new(q.shape, dtype=q.dtype, device=q.device)
-    lse = new(q.shape[:-1], dtype=torch.float32, device=q.device) if save else None
-    p = AttentionProblem(*fields, *st, *_rows(out, q, q.shape, "out"))
+    given = out is not None
+    if not given:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if save else None
+    p = AttentionProblem(*fields, 0 if given else 1, 0, *st, *_rows(out, q, q.shape, "out"))
+    if given and save and q_starts is not None:
+        lse.zero_()
     if workspace is None:
         need = hclrmix_attention_workspace_size(p)
         workspace = _scratch(None, need, q.device)
@@ -232,13 +234,13 @@ def attention_backward(q, k, v, out, lse, d_out, *, causal=True, window=0, sinks
     if lse.dtype is not torch.float32 or lse.device != q.device or lse.shape != q.shape[:-1]:
         _refuse(f"lse must be float32 {tuple(q.shape[:-1])} on the tensors' device")
     st += _rows(out, q, q.shape, "out") + _rows(d_out, q, q.shape, "d_out")
-    if grads is None:
-        new = torch.empty if q_starts is None else torch.zeros
-        grads = [new(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v)]
+    given = grads is not None
+    if not given:
+        grads = [torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v)]
     dq, dk, dv = grads
     for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
         st += (0, 0, 0) if t is None else _rows(t, q, like.shape, name)
-    p = AttentionProblem(*fields, *st, *_row_strides(lse.shape, lse.stride(), "lse"))
+    p = AttentionProblem(*fields, 0 if given else 1, 0, *st, *_row_strides(lse.shape, lse.stride(), "lse"))
     if workspace is None:
         need = hclrmix_attention_backward_workspace_size(p)
         workspace = _scratch(None, need, q.device)

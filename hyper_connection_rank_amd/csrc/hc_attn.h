@@ -37,10 +37,21 @@ struct AttnArgs {
   float* partial;
   int splits;
   int tiles;                   // row tiles (of a sequence; packed: at most, of all)
+  int zero_rest;               // packed: rows of no sequence become zeros
 };
 
 hipError_t launch_attention(AttnArgs a, int dtype, bool aligned, hipStream_t s);
 size_t attention_scratch(const AttnArgs& a, int dtype);
+// Zeros to the rows of packed tensors that belong to no sequence.
+struct RestTensor {
+  void* p;
+  Strides3 s;
+  int64_t tokens;
+  int heads, dim;
+  const int* starts;
+};
+hipError_t launch_zero_rest(const RestTensor* tensors, int n, int batch, int element, hipStream_t s);
+
 hipError_t launch_attention_backward(AttnArgs a, int dtype, bool aligned, hipStream_t s);
 size_t attention_backward_scratch(const AttnArgs& a, int dtype);
 
@@ -305,8 +316,23 @@ constexpr float LAG = 8.0f;
 // Which keys a query sees: j with lo <= j <= hi or j < first.
 struct Sees {
   int lo, hi, first;
-  __device__ __forceinline__ bool operator()(int j) const { return (j >= lo && j <= hi) || j < first; }
 };
+// Keeps x where its row's key is seen: the registers' keys are j0 + 8 (e / 4) + e % 4 (j0 with the lane's part). Away from
+// the first tokens (none) one unsigned comparison an element.
+__device__ __forceinline__ void hide_keys(f32x16& x, const Sees& s, int j0, bool none, float hidden) {
+  const uint32_t from = (uint32_t)(j0 - s.lo), span = s.hi >= s.lo ? (uint32_t)(s.hi - s.lo) + 1u : 0u;
+  if (none) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = from + (uint32_t)(8 * (e >> 2) + (e & 3)) < span ? x[e] : hidden;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int k = 8 * (e >> 2) + (e & 3);
+      const bool window = from + (uint32_t)k < span, sink = j0 + k < s.first;
+      x[e] = window | sink ? x[e] : hidden;
+    }
+  }
+}
 __device__ __forceinline__ Sees sees(const AttnArgs& a, int p, int k_len) {
   Sees s;
   const int last = a.causal ? min(p, k_len - 1) : k_len - 1;

@@ -22,7 +22,7 @@ template <DT D, int NB> struct FwdShape {
 };
 
 template <DT D, int NB, bool ALN>
-__global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? 2 : 1)) void k_attention(const AttnArgs a) {
+__global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? (NB == 2 ? 3 : 2) : 1)) void k_attention(const AttnArgs a) {
   typedef FwdShape<D, NB> F;
   typedef Rows<D, NB> T;
   typedef typename T::piece piece;
@@ -37,8 +37,9 @@ __global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? 2 : 1)) void
   // Workgroup -> key head and tile of rows. Consecutive ids go to the XCDs in turn: neighbouring heads to different
   // ones, a head's tiles (which share its keys in an L2) to as few as there are. Late tiles first: with a causal
   // mask they have the most keys.
-  const int kvh = blockIdx.x % a.kv_heads;
-  const int64_t t = (int64_t)(gridDim.x / a.kv_heads) - 1 - blockIdx.x / a.kv_heads;
+  const int all = gridDim.x / a.splits, part = blockIdx.x / all, id = blockIdx.x - part * all;
+  const int kvh = id % a.kv_heads;
+  const int64_t t = (int64_t)(all / a.kv_heads) - 1 - id / a.kv_heads;
   const Seq s = find_sequence(a, a.q_starts, a.q_tokens, a.group, F::TR, t);
   const int rows = s.ql * a.group, r0 = s.tile * F::TR;
   if (s.tile < 0 || r0 >= rows) return;
@@ -60,7 +61,10 @@ __global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? 2 : 1)) void
   }
   const Sees wg_first = sees(a, r0 / a.group + off, s.kl);
   const Sees wg_last = sees(a, min(r0 + F::TR - 1, rows - 1) / a.group + off, s.kl);
-  const KeyTiles tiles = key_tiles<KT>(wg_first, wg_last);
+  const KeyTiles range = key_tiles<KT>(wg_first, wg_last);
+  // This part's tiles of keys.
+  const int i0 = (int)((int64_t)range.count * part / a.splits), n_tiles = (int)((int64_t)range.count * (part + 1) / a.splits) - i0;
+  auto tiles = [&](int i) { return range(i0 + i); };
   const Sees w_first = sees(a, min(r0 + wave * QB * 32, rows - 1) / a.group + off, s.kl);
   const Sees w_last = sees(a, min(r0 + (wave * QB + QB) * 32 - 1, rows - 1) / a.group + off, s.kl);
 
@@ -101,10 +105,7 @@ __global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? 2 : 1)) void
     for (int b = 0; b < QB; ++b) {
       if (!whole) {
 #pragma unroll
-        for (int k = 0; k < KB; ++k)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            x[k][b][e] = see[b](j0 + 32 * k + 8 * (e >> 2) + 4 * h + (e & 3)) ? x[k][b][e] : NEG_INF;
+        for (int k = 0; k < KB; ++k) hide_keys(x[k][b], see[b], j0 + 32 * k + 4 * h, j0 >= w_last.first, NEG_INF);
       }
       float top = x[0][b][0];
 #pragma unroll
@@ -163,12 +164,12 @@ __global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? 2 : 1)) void
       ks.load(k_at(j0), ldk, n, a.dim, to, wave);
       vs.load(v_at(j0), ldv, n, a.dim, to + S::BYTES, wave);
     };
-    if (tiles.count > 0) stage(0);
-    for (int i = 0; i < tiles.count; ++i) {
+    if (n_tiles > 0) stage(0);
+    for (int i = 0; i < n_tiles; ++i) {
       // Tile i has arrived, and every wave is done with tile i - 1, whose buffer tile i + 1 fills.
       wait_loads<0>();
       lds_barrier();
-      if (i + 1 < tiles.count) stage(i + 1);
+      if (i + 1 < n_tiles) stage(i + 1);
       const unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
       multiply(cur, cur + S::BYTES, tiles(i) * KT);
     }
@@ -179,18 +180,49 @@ __global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? 2 : 1)) void
       S::fetch(k_at(j0), ldk, n, a.dim, tid, fk);
       S::fetch(v_at(j0), ldv, n, a.dim, tid, fv);
     };
-    if (tiles.count > 0) fetch(0);
-    for (int i = 0; i < tiles.count; ++i) {
+    if (n_tiles > 0) fetch(0);
+    for (int i = 0; i < n_tiles; ++i) {
       unsigned char* cur = lds + (i & 1) * 2 * S::BYTES;
       S::put(cur, tid, fk);
       S::put(cur + S::BYTES, tid, fv);
       lds_barrier();
-      if (i + 1 < tiles.count) fetch(i + 1);
+      if (i + 1 < n_tiles) fetch(i + 1);
       multiply(cur, cur + S::BYTES, tiles(i) * KT);
     }
   }
   lds_barrier();
 
+  if (a.splits > 1) {
+    // fp32 sums as they are, [part][row of q][head][dim], then their maxima and sums of weights.
+    const int64_t heads_all = (a.q_starts ? a.q_tokens : a.batch * a.q_tokens) * a.heads;
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      const int r = r0 + (wave * QB + b) * 32 + (lane & 31), tok = r / a.group;
+      const float total = halves_sum(l[b]);
+      if (r >= rows) continue;
+      const int64_t at = part * heads_all + ((a.q_starts ? s.q0 : s.b * a.q_tokens) + tok) * a.heads + kvh * a.group + r - tok * a.group;
+      float* const to = a.partial + at * a.dim;
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int col = 32 * d + 8 * u + 4 * h;
+          if (ALN) {  // dim is a multiple of four
+            if (col < a.dim) *(f32x4*)(to + col) = f32x4{o[b][d][4 * u], o[b][d][4 * u + 1], o[b][d][4 * u + 2], o[b][d][4 * u + 3]};
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col + e < a.dim) to[col + e] = o[b][d][4 * u + e];
+          }
+        }
+      if (h == 0) {
+        float* const st = a.partial + a.splits * heads_all * a.dim + at * 2;
+        st[0] = m[b];
+        st[1] = total;
+      }
+    }
+    return;
+  }
   // O^T through LDS (each wave its own part), so that rows are written 16 bytes a lane.
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
@@ -216,7 +248,80 @@ __global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? 2 : 1)) void
   }
 }
 
+// The parts of every row and head joined in ascending order, one wave for each.
+template <DT D> __global__ __launch_bounds__(256) void k_attention_parts(const AttnArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = a.q_starts ? a.q_tokens : a.batch * a.q_tokens, all = rows * a.heads;
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (at >= all) return;
+  const int64_t row = at / a.heads;
+  const int head = (int)(at - row * a.heads);
+  if (a.q_starts && (row < a.q_starts[0] || row >= a.q_starts[a.batch])) return;
+  const float* const st = a.partial + a.splits * all * a.dim;
+  // Part p's maximum and sum in lane p (at most 32 parts).
+  const float m = lane < a.splits ? st[(lane * all + at) * 2] : NEG_INF;
+  float top = m;
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  const float f = m == NEG_INF ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+  const float part = lane < a.splits ? f * st[(lane * all + at) * 2 + 1] : 0.0f;
+  float total = 0.0f, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int p = 0; p < a.splits; ++p) {
+    const float w = __shfl(f, p, 64);
+    total = total + __shfl(part, p, 64);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (lane + 64 * i < a.dim) y[i] = y[i] + w * a.partial[(p * all + at) * a.dim + lane + 64 * i];
+  }
+  const int64_t b = a.q_starts ? 0 : row / a.q_tokens, t = row - b * a.q_tokens;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lane + 64 * i < a.dim)
+      hc::st<D>(a.out, b * a.so.b + t * a.so.t + head * a.so.h + lane + 64 * i, total == 0.0f ? 0.0f : y[i] / total);
+  if (a.lse && lane == 0)
+    a.lse[b * a.sl.b + t * a.sl.t + head * a.sl.h] =
+        total == 0.0f ? NEG_INF : (top - weight_shift<D>() + __builtin_amdgcn_logf(total)) * LN2;
+}
+
+struct Rest {
+  RestTensor t[3];
+  int batch;
+};
+template <typename E> __global__ __launch_bounds__(256) void k_zero_rest(const Rest a) {
+  const RestTensor& x = a.t[blockIdx.y];
+  if (!x.p) return;
+  const int64_t first = min(max((int64_t)x.starts[0], (int64_t)0), x.tokens);
+  const int64_t end = min(max((int64_t)x.starts[a.batch], first), x.tokens);
+  const int64_t per = (int64_t)x.heads * x.dim, n = (first + x.tokens - end) * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / per, row = r < first ? r : r - first + end;
+    const int c = (int)(i - r * per), head = c / x.dim;
+    ((E*)x.p)[row * x.s.t + head * x.s.h + c - head * x.dim] = 0;
+  }
+}
+
+// How many rows are behind the last sequence only the device knows: a small grid that takes them in turn.
+hipError_t launch_zero_rest(const RestTensor* tensors, int n, int batch, int element, hipStream_t s) {
+  Rest a{};
+  a.batch = batch;
+  for (int i = 0; i < n; ++i) a.t[i] = tensors[i];
+  if (element == 4) hipLaunchKernelGGL(k_zero_rest<uint32_t>, dim3(128, n), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(k_zero_rest<uint16_t>, dim3(128, n), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
 namespace {
+
+// Few tiles of rows: their keys are split over up to 32 workgroups each, of at least four tiles of 64 keys, until there are
+// two workgroups for every compute unit.
+constexpr int64_t MOST_SPLITS = 32, FEW = 256, ENOUGH = 512, ROW_TILE = 128;
+int key_splits(const AttnArgs& a, int64_t groups) {
+  if (groups >= FEW) return 1;
+  int64_t keys = a.k_tokens;
+  if (a.window) keys = std::min(keys, (int64_t)(a.causal ? 1 : 2) * a.window + a.sinks + ROW_TILE / a.group);
+  return (int)std::max<int64_t>(1, std::min({MOST_SPLITS, (ENOUGH + groups - 1) / groups, keys / 256}));
+}
 
 template <DT D, int NB> hipError_t go(const AttnArgs& a0, bool aligned, hipStream_t s) {
   typedef FwdShape<D, NB> F;
@@ -228,9 +333,15 @@ template <DT D, int NB> hipError_t go(const AttnArgs& a0, bool aligned, hipStrea
     a.tiles = (int)((rows + F::TR - 1) / F::TR);
     tiles = (int64_t)a.tiles * a.batch;
   }
-  const dim3 grid((unsigned)(tiles * a.kv_heads)), block(64 * F::WAVES);
+  static_assert(F::TR == ROW_TILE, "key_splits counts in these tiles");
+  a.splits = key_splits(a, tiles * a.kv_heads);
+  const dim3 grid((unsigned)(tiles * a.kv_heads * a.splits)), block(64 * F::WAVES);
   if (aligned) hipLaunchKernelGGL((k_attention<D, NB, true>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((k_attention<D, NB, false>), grid, block, 0, s, a);
+  if (a.splits > 1) {
+    const int64_t n = (a.q_starts ? a.q_tokens : a.batch * a.q_tokens) * a.heads;
+    hipLaunchKernelGGL(k_attention_parts<D>, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 
@@ -251,6 +362,13 @@ hipError_t launch_attention(AttnArgs a, int dtype, bool aligned, hipStream_t s) 
   }
 }
 
-size_t attention_scratch(const AttnArgs&, int) { return 0; }
+// Parts of at most ENOUGH workgroups' rows beside one of all of fewer than FEW workgroups' rows, whatever the masks: with
+// fewer sequences, rows or keys no more.
+size_t attention_scratch(const AttnArgs& a, int) {
+  const int64_t rows = (a.q_starts ? a.q_tokens : a.batch * a.q_tokens) * a.heads;
+  const int64_t most = std::min(MOST_SPLITS, a.k_tokens / 256);
+  if (most < 2) return 0;
+  return (size_t)std::min(most * rows, ENOUGH * ROW_TILE + std::min(rows, FEW * ROW_TILE)) * ((size_t)a.dim + 2) * sizeof(float);
+}
 
 }  // namespace hc

@@ -144,11 +144,11 @@ int held(int x) { return std::min(x, 1 << 29); }
 
 hclrmix_status check_attention(const hclrmix_attention_problem* p) {
   if (!p) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem must not be NULL");
-  if (p->reserved[0] || p->reserved[1]) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem.reserved must be 0");
+  if (p->reserved) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "problem.reserved must be 0");
   if (hclrmix_status st = check_heads(p->dtype, p->heads, p->kv_heads, p->dim)) return st;
   if (hclrmix_status st = check_mask(p->window, p->sinks, p->scale)) return st;
-  if (p->causal < 0 || p->causal > 1 || p->packed < 0 || p->packed > 1)
-    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "causal and packed must be 0 or 1");
+  if (p->causal < 0 || p->causal > 1 || p->packed < 0 || p->packed > 1 || p->zero_rest < 0 || p->zero_rest > 1)
+    return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "causal, packed and zero_rest must be 0 or 1");
   if (p->batch < 0 || p->q_tokens < 0 || p->k_tokens < 0)
     return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "batch and tokens must be >= 0");
   if (p->batch > HCLRMIX_ATTENTION_MAX_BATCH || p->q_tokens > HCLRMIX_MAX_ROWS || p->k_tokens > HCLRMIX_MAX_ROWS)
@@ -274,7 +274,8 @@ hclrmix_status hclrmix_attention(const void* q, const void* k, const void* v, co
   if (hclrmix_status st = view(vk, "k", k, p.k, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
   if (hclrmix_status st = view(vv, "v", v, p.v, e.n, e.k, p.kv_heads, p.dim, es, false)) return st;
   if (hclrmix_status st = view(vo, "out", out, p.out, e.n, e.q, p.heads, p.dim, es, true)) return st;
-  if (p.batch == 0 || p.q_tokens == 0) return ok();
+  const bool rest = p.packed && p.zero_rest;  // also of no sequences
+  if (p.q_tokens == 0 || (p.batch == 0 && !rest)) return ok();
   if (!q || !out || (p.k_tokens > 0 && (!k || !v)))
     return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "q, k, v and out are required");
   const size_t need = attention_need(problem);
@@ -297,6 +298,12 @@ hclrmix_status hclrmix_attention(const void* q, const void* k, const void* v, co
   a.sl = strides(vl);
   a.partial = (float*)((char*)workspace + HCLRMIX_COUNTER_BYTES);
   (void)hipGetLastError();
+  if (rest) {
+    const hc::RestTensor tensors[2] = {{out, a.so, p.q_tokens, p.heads, p.dim, a.q_starts},
+                                    {lse, hc::Strides3{0, a.sl.t * (int64_t)(4 / es), a.sl.h * (int64_t)(4 / es)}, p.q_tokens, p.heads, (int)(4 / es), a.q_starts}};
+    if (hipError_t e = hc::launch_zero_rest(tensors, lse ? 2 : 1, a.batch, (int)es, (hipStream_t)stream)) return done(e);
+    if (p.batch == 0) return ok();
+  }
   return done(hc::launch_attention(a, p.dtype, aligned16({&vq, &vk, &vv, &vo}), (hipStream_t)stream));
 }
 
@@ -308,7 +315,6 @@ hclrmix_status hclrmix_attention_backward(const void* q, const void* k, const vo
   if (hclrmix_status st = check_attention(problem)) return st;
   const hclrmix_attention_problem& p = *problem;
   if (hclrmix_status st = check_starts(p, q_starts, k_starts)) return st;
-  if (!dq && !dk && !dv) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "no gradient is wanted");
   const size_t es = elem_size(p.dtype);
   const Extent e = extent(p);
   View vq, vk, vv, vo, vg, vl, wq, wk, wv;
@@ -321,7 +327,9 @@ hclrmix_status hclrmix_attention_backward(const void* q, const void* k, const vo
   if (hclrmix_status st = view(wq, "dq", dq, p.dq, e.n, e.q, p.heads, p.dim, es, true)) return st;
   if (hclrmix_status st = view(wk, "dk", dk, p.dk, e.n, e.k, p.kv_heads, p.dim, es, true)) return st;
   if (hclrmix_status st = view(wv, "dv", dv, p.dv, e.n, e.k, p.kv_heads, p.dim, es, true)) return st;
-  if (p.batch == 0 || (p.q_tokens == 0 && p.k_tokens == 0)) return ok();
+  const bool rest = p.packed && p.zero_rest;  // also of no sequences
+  if ((p.q_tokens == 0 && p.k_tokens == 0) || (p.batch == 0 && !rest)) return ok();
+  if (!dq && !dk && !dv) return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "no gradient is wanted");
   if ((p.q_tokens > 0 && (!q || !out || !d_out || !lse)) || (p.k_tokens > 0 && (!k || !v)))
     return fail(HCLRMIX_ERR_INVALID_ARGUMENT, "q, k, v, out, lse and d_out are required");
   const size_t need = attention_backward_need(problem);
@@ -352,6 +360,13 @@ hclrmix_status hclrmix_attention_backward(const void* q, const void* k, const vo
   a.sdv = strides(wv);
   a.stats = (float*)((char*)workspace + HCLRMIX_COUNTER_BYTES);
   (void)hipGetLastError();
+  if (rest) {
+    const hc::RestTensor tensors[3] = {{dq, a.sdq, p.q_tokens, p.heads, p.dim, a.q_starts},
+                                    {dk, a.sdk, p.k_tokens, p.kv_heads, p.dim, a.k_starts},
+                                    {dv, a.sdv, p.k_tokens, p.kv_heads, p.dim, a.k_starts}};
+    if (hipError_t e = hc::launch_zero_rest(tensors, 3, a.batch, (int)es, (hipStream_t)stream)) return done(e);
+    if (p.batch == 0) return ok();
+  }
   return done(hc::launch_attention_backward(a, p.dtype, aligned16({&vq, &vk, &vv, &vo, &vg, &wq, &wk, &wv}), (hipStream_t)stream));
 }
 

@@ -68,7 +68,7 @@ template <DT D, int NB> struct DqShape {
 };
 
 template <DT D, int NB, bool ALN>
-__global__ __launch_bounds__(256, 1) void k_attention_dq(const AttnArgs a) {
+__global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? (NB == 2 ? 3 : 2) : 1)) void k_attention_dq(const AttnArgs a) {
   typedef DqShape<D, NB> F;
   typedef Rows<D, NB> T;
   typedef typename T::piece piece;
@@ -154,10 +154,7 @@ __global__ __launch_bounds__(256, 1) void k_attention_dq(const AttnArgs a) {
       for (int i = 0; i < STEPS; ++i) y = mfma32<D>(T::direct(vt, 32 * k, i, lane), go[i], y);
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], c, -lse2)) * (y[e] - delta);
-      if (!whole) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = see(i0 + 8 * (e >> 2) + 4 * h + (e & 3)) ? x[e] : 0.0f;
-      }
+      if (!whole) hide_keys(x, see, i0 + 4 * h, i0 >= w_last.first, 0.0f);
       scale.apply(x, dq);
 #pragma unroll
       for (int i = 0; i < PSTEPS; ++i) {
@@ -308,8 +305,8 @@ __global__ __launch_bounds__(256, (ALN ? DkvShape<D, NB>::WAVES : 1)) void k_att
   const int low = a.causal ? 0 : any ? -(1 << 30) : 1 - a.window;
   const uint32_t span = any ? 0x7FFFFFFFu : (uint32_t)(a.window - low);
 
-  // A tile whose queries start at t0. The sums start from what is subtracted in any case: s - lse, over the scale, and
-  // dP - delta.
+  // A tile whose queries start at t0. In 16 bits the sums start from what is subtracted in any case: s - lse, over the scale,
+  // and dP - delta. (fp32 would lose accuracy: every addition would round relative to lse over the scale.)
   auto multiply = [&](auto buffer, int t0) {
     constexpr int buf = decltype(buffer)::value;
     const unsigned char* const qt = lds + buf * 2 * S::BYTES;
@@ -320,18 +317,24 @@ __global__ __launch_bounds__(256, (ALN ? DkvShape<D, NB>::WAVES : 1)) void k_att
     const bool whole = (!a.causal || jz <= pa) &&
                        (!a.window || (jw > pz - a.window && (a.causal || jz < pa + a.window)) || jz < a.sinks);
     f32x16 x[RBW], y[RBW];
-#pragma unroll
-    for (int b = 0; b < RBW; ++b)
+    auto statistic = [&](int which, int b, f32x16& to) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const f32x4 sl = *(const f32x4*)&row_stats[buf][0][32 * b + 8 * u + 4 * h];
-        const f32x4 dl = *(const f32x4*)&row_stats[buf][1][32 * b + 8 * u + 4 * h];
+        const f32x4 v = *(const f32x4*)&row_stats[buf][which][32 * b + 8 * u + 4 * h];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[b][4 * u + e] = sl[e];
-          y[b][4 * u + e] = dl[e];
-        }
+        for (int e = 0; e < 4; ++e) to[4 * u + e] = v[e];
       }
+    };
+#pragma unroll
+    for (int b = 0; b < RBW; ++b) {
+      if constexpr (D == DT::F32) {
+        clear(x[b]);
+        clear(y[b]);
+      } else {
+        statistic(0, b, x[b]);
+        statistic(1, b, y[b]);
+      }
+    }
 #pragma unroll
     for (int b = 0; b < RBW; ++b)
 #pragma unroll
@@ -340,10 +343,23 @@ __global__ __launch_bounds__(256, (ALN ? DkvShape<D, NB>::WAVES : 1)) void k_att
     for (int b = 0; b < RBW; ++b)
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) y[b] = mfma32<D>(T::direct(gt, 32 * b, i, lane), vf[i], y[b]);
+    if constexpr (D == DT::F32) {
+#pragma unroll
+      for (int b = 0; b < RBW; ++b) {
+        f32x16 sl, dl;
+        statistic(0, b, sl);
+        statistic(1, b, dl);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[b][e] = fmaf(x[b][e], c, sl[e] * c);
+          y[b][e] = y[b][e] + dl[e];
+        }
+      }
+    }
 #pragma unroll
     for (int b = 0; b < RBW; ++b)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[b][e] = __builtin_amdgcn_exp2f(x[b][e] * c);
+      for (int e = 0; e < 16; ++e) x[b][e] = __builtin_amdgcn_exp2f(D == DT::F32 ? x[b][e] : x[b][e] * c);
     if (!whole) {
       const uint32_t from = (uint32_t)(pa + 4 * h - j - low);
 #pragma unroll

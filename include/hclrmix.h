@@ -519,7 +519,8 @@ typedef struct {
   int32_t sinks;     /* first keys outside the window that stay visible; without a window of no effect */
   int32_t packed;    /* 1: sequences lie one after another, at starts */
   float scale;       /* > 0 */
-  int32_t reserved[2];                  /* must be 0 */
+  int32_t zero_rest;  /* packed: 1 writes zeros to the outputs' rows that belong to no sequence, 0 leaves them */
+  int32_t reserved;   /* must be 0 */
   hclrmix_strides q, k, v, out;         /* .sequence is not used of packed tensors */
   hclrmix_strides d_out, dq, dk, dv;    /* backward only */
   hclrmix_strides lse;                  /* [sequence][token][head], in floats */
@@ -530,8 +531,9 @@ typedef struct {
  * receives the logarithms that the backward pass takes.
  * Packed: q_starts [batch + 1] int32 device memory, ascending: sequence b's
  * queries are rows q_starts[b] to q_starts[b + 1] - 1; k_starts likewise for
- * keys, or NULL where they are the same. Rows outside every sequence are
- * neither read nor written. Not packed: both NULL.
+ * keys, or NULL where they are the same. Rows before the first and behind
+ * the last sequence are not read, and not written but for zero_rest. Not
+ * packed: both NULL.
  * rows and heads: tokens of all sequences times heads at most 2^29, batch
  * times heads at most 2^20. */
 hclrmix_status hclrmix_attention(const void* q, const void* k, const void* v, const int32_t* q_starts,

@@ -5,7 +5,10 @@ U, F and ``within`` as in ``_ffn``. The bounds add up, for one query:
    products + |s|) times the scale (see ``_ffn.product``); then the factor
    log2 e, the subtraction of the maximum (or of lse, itself multiplied) and
    the exponential, whose errors are relative to the exponents: 8 F (|s| +
-   |m| + 1). So a weight's relative error is below e_j.
+   |m| + 1). So a weight's relative error is below e_j. The backward pass of
+   16-bit types starts the sums of s and dP from -lse over the scale and
+   -delta: their dim additions round relative to those too, 8 F sqrt(dim)
+   (|lse| and |delta|) more.
  - weights rounded to T as 16-bit operands: every term of the sum over keys
    moves by an independent error with standard deviation below
    U |term| / sqrt(3); 4 U norm2(terms) is 6.9 of them. fp16 weights are kept
@@ -82,16 +85,16 @@ def head_backward(q, k, v, out, lse, do, see, scale, dt):
     es = 8 * F * r * (scale * n2(q, k.t()) + s.abs())
     l0 = lse.masked_fill(lse == -math.inf, 0.0)[:, None]
     p = torch.exp(s - l0).masked_fill(~see, 0.0)
-    e = es + 8 * F * (s.abs() + l0.abs() + 1)
+    low = dt != torch.float32
+    e = es + 8 * F * (s.abs() + l0.abs() + 1) + (8 * F * r * l0.abs() if low else 0)
     dp = do @ v.t()
     edp = 8 * F * r * (n2(do, v.t()) + dp.abs())
     delta = (out * do).sum(1, keepdim=True)
-    edl = 8 * F * r * (torch.sqrt((out * out * do * do).sum(1, keepdim=True)) + delta.abs())
+    edl = 8 * F * r * (torch.sqrt((out * out * do * do).sum(1, keepdim=True)) + (2 if low else 1) * delta.abs())
     t = dp - delta
     ds = p * t
     seen = see.double()
     eds = p * (e * t.abs() + edp + edl + 4 * F * (dp.abs() + delta.abs())) + LEAST * seen * (1 + t.abs())
-    low = dt != torch.float32
 
     def total(a, ea, b, small):
         """a^T b summed over a's rows, its bound; small: the absolute rounding of an operand that leaves the normal numbers."""

@@ -103,10 +103,13 @@ def test_attention_limits():
 
 @pytest.mark.parametrize("name", WHOLE)
 def test_attention_reserved(name):
-    for i in range(2):
+    c = Call(name)
+    c.problem.reserved = 1
+    expect(c, E, "reserved")
+    for x in (-1, 2):
         c = Call(name)
-        c.problem.reserved[i] = 1
-        expect(c, E, "reserved")
+        c.problem.zero_rest = x
+        expect(c, E, "zero_rest")
 
 
 @pytest.mark.parametrize("name,missing", [(n, m) for n in WHOLE for m in ("q", "k", "v", "out")] +

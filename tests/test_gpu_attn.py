@@ -91,6 +91,38 @@ def test_packed_sequences(dt, lens):
 
 
 @pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("ql,kl,heads,kv,dim", [(1, 5000, 4, 1, 64), (7, 3100, 3, 3, 128), (40, 2100, 5, 1, 57), (1, 9000, 1, 1, 256), (200, 1030, 2, 1, 96)])
+def test_few_queries_over_many_keys(dt, ql, kl, heads, kv, dim):
+    """The keys split over workgroups, whose parts are joined; some of them see nothing."""
+    for mask in (dict(), dict(causal=False), dict(window=600, sinks=5), dict(window=2000)):
+        check(*make(dt, 2, ql, kl, heads, kv, dim), f"{dt} {ql} {kl} {dim} {mask}", **mask)
+    t = T_OF[dt]
+    lens_q, lens_k = [ql, 0, 1, 3], [kl, 700, 1, 0]
+    q, k, v = rand((sum(lens_q) + 2, heads, dim), t, 1), rand((sum(lens_k), kv, dim), t, 2), rand((sum(lens_k), kv, dim), t, 3)
+    check(q, k, v, f"{dt} {ql} {kl} {dim} packed", ql=lens_q, kl=lens_k)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_no_sequences(dt):
+    t = T_OF[dt]
+    x = [rand((9, h, 64), t, h) for h in (4, 2, 2)]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = hc.attention(*x, save=True, q_starts=st)
+    assert not out.any() and not lse.any()
+    assert not any(g.any() for g in hc.attention_backward(*x, out, lse, x[0], q_starts=st))
+    empty = [y[:0] for y in x]
+    out, lse = hc.attention(*empty, save=True)
+    assert out.shape == (0, 4, 64)
+    assert [g.shape for g in hc.attention_backward(*empty, out, lse, empty[0])] == [y.shape for y in empty]
+    out, lse = hc.attention(x[0], x[1][:0], x[2][:0], save=True)
+    assert not out.any() and (lse == -math.inf).all()
+    assert not hc.attention_backward(x[0], x[1][:0], x[2][:0], out, lse, x[0])[0].any()
+    out, lse = hc.attention(x[0][:0], *x[1:], save=True)
+    dq, dk, dv = hc.attention_backward(x[0][:0], *x[1:], out, lse, x[0][:0])
+    assert not dk.any() and not dv.any()
+
+
+@pytest.mark.parametrize("dt", TYPES)
 def test_packed_sequences_with_other_key_lengths(dt):
     ql, kl = [3, 0, 70, 1, 200], [40, 9, 70, 0, 90]
     t = T_OF[dt]

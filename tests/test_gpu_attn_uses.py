@@ -176,7 +176,8 @@ def test_training_in_graphs(dt):
     graphs = []
     for i in range(2):
         x = inputs(i)
-        ws = torch.zeros(hc.attention_workspace_size(4, n, n, heads, kv, dim, t, packed=True, backward=True), dtype=torch.uint8, device="cuda")
+        ws = torch.zeros(max(hc.attention_workspace_size(4, n, n, heads, kv, dim, t, packed=True, backward=b) for b in (False, True)),
+                         dtype=torch.uint8, device="cuda")
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
