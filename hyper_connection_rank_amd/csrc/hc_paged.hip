@@ -15,6 +15,8 @@ namespace hc {
 // after one key of every block of 16: it finds the key's page, loads 16 bytes in every 64 of the key's row of k, as
 // the matrix op wants them, and of its row of v, which goes to LDS directly to be read transposed. The cache's
 // rows are read once; they bound the kernel, so two tiles of every wave are on their way or in work at all times.
+// Measured: 64 sequences of 1 to 16384 keys, 20/4 heads of 128 in bf16, 217 us (983 MB, 4.5 TB/s; loading alone takes as long),
+// the join of the parts 6; one of 32768 keys, 32/8 heads, 28 us (4.8 TB/s) and 6.
 
 typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
 
@@ -420,7 +422,8 @@ size_t paged_scratch(const PagedArgs& a, int dtype) {
 
 // ------------------------------------------------------------------ rows into the cache
 
-// One thread per 16 bytes of a row (aligned) or per element. Bound by HBM, or by the launch for a step's tokens.
+// One thread per 16 bytes of a row (aligned) or per element. Bound by HBM (16084 rows of 8 heads of 128 in bf16: 20 us, 6.6
+// TB/s), or by the launch for a step's tokens (2.7 us).
 template <typename E> __global__ __launch_bounds__(256) void k_store(const StoreArgs a, int per_head) {
   const int64_t n = a.tokens * a.kv_heads * per_head;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
