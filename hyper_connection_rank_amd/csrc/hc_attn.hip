@@ -21,11 +21,10 @@ template <DT D, int NB> struct FwdShape {
   static constexpr int WAVES = 4, QB = 1, TR = 32 * QB * WAVES;
 };
 
-// Bound by the matrix units and the vector units together at the power limit: 8192 tokens, 32/8 heads of 128 in bf16, causal,
-// 560 us (980 TFLOP/s, 1.9 GHz): matrix ops take 49 % of the cycles and about 6.7 vector instructions per 64 scores most of the
-// others. Two workgroups of 128 rows a compute unit (64 KB of LDS, 230 registers): in 276 registers one fits, 940 us.
-// Narrow windows are bound by the tiles that the mask crosses and each workgroup's start: 14292 packed tokens, 20/4
-// heads of 64 in fp16, window 512, 65 us (29.7 GFLOP).
+// Bound by the matrix and the vector units together: 8192 tokens, 32/8 heads of 128 in bf16, causal, 530-640 us from run to run
+// (560: 980 TFLOP/s); matrix ops are busy in 49 % of the cycles, with 6.7 vector instructions per 64 scores beside them.
+// Registers are held to two workgroups of 128 rows a compute unit (64 KB of LDS, 227 registers): with one 895-931 us, with two
+// 565-620. 14292 packed tokens, 20/4 heads of 64 in fp16, window 512: 65 us (29.7 GFLOP, matrix ops busy in 22 %).
 template <DT D, int NB, bool ALN>
 __global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? (NB == 2 ? 3 : 2) : 1)) void k_attention(const AttnArgs a) {
   typedef FwdShape<D, NB> F;

@@ -60,8 +60,9 @@ __device__ __forceinline__ void clear(f32x16& x) {
   for (int e = 0; e < 16; ++e) x[e] = 0.0f;
 }
 
-// Measured: 2 x 4096 tokens, 20/4 heads of 128 in bf16, causal: dq 270 us (258 GFLOP, 950 TFLOP/s), dk and dv 455 (344
-// GFLOP) and their join 20; 9 sequences of up to 1501, 12 heads of 80 in fp16, window 300: 48 and 73 us.
+// Measured: 2 x 4096 tokens, 20/4 heads of 128 in bf16, causal: dq 283 us (258 GFLOP, 910 TFLOP/s), dk and dv 473 (344
+// GFLOP, 730 TFLOP/s) and their join 21 (medians under a trace); 9 sequences of up to 1501, 12 heads of 80 in fp16, window 300:
+// 51 and 78 us.
 
 // ------------------------------------------------------------------ dq
 
@@ -230,10 +231,9 @@ __global__ __launch_bounds__(256, (D != DT::F32 && NB <= 4 && ALN ? (NB == 2 ? 3
 // works on RBW = 2 blocks of 32 rows at once, which fill each other's gaps.
 // NBO: blocks of 32 columns of dk and dv that one workgroup sums (all, or half where the registers hold no more).
 //
-// What was slower at 128 columns in bf16 (the same case, dk and dv): one block of rows a wave 650 us, with its products in a
-// pipeline over four buffers 470 (half the tiles of keys); two waves for each block of keys, one for dv and one for dk,
-// 450 in three parts, 810 in one; v's rows from LDS to fit two waves a SIMD 680 (registers spill); two blocks of keys
-// a wave 755 (spills).
+// What was slower at 128 columns in bf16 (the same case, dk and dv): one block of rows a wave, rows not split, 658 us;
+// two waves for each block of keys, one for dv and one for dk, 810; v's rows from LDS to fit two waves a SIMD 681 (registers
+// spill); two blocks of keys a wave 757 (spills).
 //
 // Few tiles of keys: the rows are split over `parts` workgroups, whose fp32 sums k_attention_join adds in order.
 template <DT D, int NB> struct DkvShape {

@@ -15,8 +15,9 @@ namespace hc {
 // after one key of every block of 16: it finds the key's page, loads 16 bytes in every 64 of the key's row of k, as
 // the matrix op wants them, and of its row of v, which goes to LDS directly to be read transposed. The cache's
 // rows are read once; they bound the kernel, so two tiles of every wave are on their way or in work at all times.
-// Measured: 64 sequences of 1 to 16384 keys, 20/4 heads of 128 in bf16, 217 us (983 MB, 4.5 TB/s; loading alone takes as long),
-// the join of the parts 6; one of 32768 keys, 32/8 heads, 28 us (4.8 TB/s) and 6.
+// Measured: 64 sequences of 1 to 16384 keys, 20/4 heads of 128 in bf16, 217 us (983 MB, 4.5 TB/s),
+// the join of the parts 6; one of 32768 keys, 32/8 heads, 28 us (4.7 TB/s) and 6. Before the heads turned
+// over the XCDs 265 us for the first, of which loading without any arithmetic took 253.
 
 typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
 
@@ -606,7 +607,7 @@ __global__ __launch_bounds__(MAP_THREADS) void k_page_map(const MapArgs a) {
   fill_maps(a, starts, taken);
 }
 
-// One launch up to 1024 requests (64 requests of one token 6.6 us in two kernels, 4 in one).
+// One launch up to 1024 requests (64 requests of one token: one kernel of 4.9 us).
 hipError_t launch_page_map(const MapArgs& a, hipStream_t s) {
   const int64_t n = std::max<int64_t>(a.tokens, a.batch);
   if (a.batch <= MAP_THREADS) {
