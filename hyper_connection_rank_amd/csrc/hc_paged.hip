@@ -607,7 +607,7 @@ __global__ __launch_bounds__(MAP_THREADS) void k_page_map(const MapArgs a) {
   fill_maps(a, starts, taken);
 }
 
-// One launch up to 1024 requests (64 requests of one token: one kernel of 4.9 us).
+// One launch up to 1024 requests (64 requests of one token: the call 14.7 us in two launches, 14.4 in one, whose kernel takes 4.9).
 hipError_t launch_page_map(const MapArgs& a, hipStream_t s) {
   const int64_t n = std::max<int64_t>(a.tokens, a.batch);
   if (a.batch <= MAP_THREADS) {

@@ -81,6 +81,19 @@ def test_windows_and_first_tokens(dt, causal, window, sinks):
 
 
 @pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("dim", [97, 127, 129, 193, 255, 256])
+def test_wide_heads_over_many_tiles(dt, dim):
+    """Sizes whose kernels hold more than the registers do, with groups, masks and packed rows over several tiles."""
+    for mask in (dict(), dict(causal=False), dict(window=150, sinks=5)):
+        check(*make(dt, 2, 333, 421, 6, 2, dim), f"{dt} {dim} {mask}", **mask)
+    lens, t = [301, 0, 1, 130], T_OF[dt]
+    n = sum(lens) + 2
+    q, k, v = rand((n, 6, dim), t, 1), rand((n, 2, dim), t, 2), rand((n, 2, dim), t, 3)
+    for mask in (dict(), dict(window=70, sinks=3)):
+        check(q, k, v, f"{dt} {dim} packed {mask}", ql=lens, **mask)
+
+
+@pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("lens", [[5], [0], [0, 0, 3], [1, 1, 1, 1], [128, 1, 129, 0, 64], [300, 2, 31, 33, 0, 0, 257, 1], [1] * 70, [3, 0] * 100])
 def test_packed_sequences(dt, lens):
     n = sum(lens) + 3
